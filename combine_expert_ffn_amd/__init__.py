@@ -18,11 +18,13 @@ from ._lib import (  # noqa: F401
     MOE_ROUTE_TOPK_FROM_LOGITS, MOE_ROUTE_FORCE_BALANCE, MOE_ACCUM_DX, MOE_ACCUM_DW,
     MOE_STEP_SERIALIZE, MOE_STEP_EAGER_WGRAD, MOE_STEP_SKIP_WGRAD, MOE_STEP_FUSED_PERMUTE,
     MOE_STEP_MID_WGRAD, MOE_STEP_FUSED_COMBINE_BWD, MOE_STEP_PAIR_WGRAD, MOE_STEP_FUSED_SCATTER,
-    MOE_STEP_GROUP4_WGRAD,
+    MOE_STEP_GROUP4_WGRAD, FP8_WEIGHT_FIELDS, MOE_FP8_BLOCK, MoeAdamwHyper, MoeAdamwTensor,
+    MoeFp8Weights,
 )
 
 
 _DATA, _F32, _I32 = "data", "f32", "i32"
+_FP8, _U8 = "fp8", "u8"
 
 
 def _torch_dtype(kind, s):
@@ -32,6 +34,10 @@ def _torch_dtype(kind, s):
         return torch.float32
     if kind == _I32:
         return torch.int32
+    if kind == _FP8:
+        return torch.float8_e4m3fn
+    if kind == _U8:
+        return torch.uint8
     return {MOE_BF16: torch.bfloat16, MOE_F16: torch.float16}.get(s.dtype, torch.float32)
 
 
@@ -434,6 +440,164 @@ def moe_dispatch_bwd(s, dxp, row_of_pair, idx, dlogits, W_r, dx, accumulate, ws,
     wp, wb = _ws(ws)
     check(lib().moe_dispatch_bwd(C.byref(s), _p(dxp), _p(row_of_pair), _p(idx), _p(dlogits),
                                  _p(W_r), _p(dx), int(accumulate), wp, wb, _stream(stream)))
+
+
+# ---- experts on 8-bit operands ----------------------------------------------
+def moe_fp8_scale_ld(k: int) -> int:
+    """Bytes per row of scales of a matrix with k values per row."""
+    return lib().moe_fp8_scale_ld(int(k))
+
+
+def moe_fp8_workspace_bytes(s: MoeShape) -> int:
+    return lib().moe_fp8_workspace_bytes(C.byref(s))
+
+
+class Fp8Weights:
+    """The routed experts' weights in 8 bits for shape ``s`` (moe_fp8_weights in
+    include/moe.h): e4m3 tensors gu, down (and transposed guT, downT) with their
+    uint8 scales.  Tensors not given are allocated; with ``transposed=False`` the
+    transposed copies, which only the dgrad reads, are left out."""
+
+    def __init__(self, s: MoeShape, device="cuda", transposed=True, **tensors):
+        import torch
+
+        d, F, E_l = s.d, s.F, s.E_l
+        given_t = any(n.startswith(("guT", "downT")) for n in tensors)
+        if tensors and not given_t:
+            transposed = False
+        for n in tensors:
+            if n not in FP8_WEIGHT_FIELDS:
+                raise ValueError(f"Fp8Weights: unknown tensor {n}")
+        b = MOE_FP8_BLOCK
+        for n, rows, k in (("gu", 2 * F, d), ("down", d, F), ("guT", d, 2 * F), ("downT", F, d)):
+            ld = (k // b + 3) // 4 * 4
+            for name, shape, kind in ((n, (E_l, rows, k), _FP8),
+                                      (n + "_s", (E_l, rows // b, ld), _U8)):
+                t = tensors.get(name)
+                if t is None and (transposed or not n.endswith("T")):
+                    t = torch.empty(shape, dtype=_torch_dtype(kind, s), device=device)
+                _chk(s, "Fp8Weights", name, t, kind, shape[0] * shape[1] * shape[2],
+                     optional=n.endswith("T"))
+                setattr(self, name, t)
+        self.shape = (d, F, E_l)
+        self.struct = MoeFp8Weights(*[_p(getattr(self, n)) for n in FP8_WEIGHT_FIELDS])
+
+    def check(self, fn, s: MoeShape):
+        if self.shape != (s.d, s.F, s.E_l):
+            raise MoeError(MOE_ERR_ARG, f"{fn}: weights are for (d, F, E_l) = {self.shape}, the "
+                                        f"shape has {(s.d, s.F, s.E_l)}")
+        return C.byref(self.struct)
+
+
+def moe_quant_rows_fp8(s, src, rows, n_rows, q, qs, stream=None):
+    """n_rows: None, or a device int32 tensor whose first element is the number
+    of rows that exist."""
+    fn, d = "moe_quant_rows_fp8", s.d
+    _chk(s, fn, "src", src, _DATA, rows * d)
+    _chk(s, fn, "n_rows", n_rows, _I32, 1, optional=True)
+    _chk(s, fn, "q", q, _FP8, rows * d)
+    _chk(s, fn, "qs", qs, _U8, rows * ((d // MOE_FP8_BLOCK + 3) // 4 * 4))
+    check(lib().moe_quant_rows_fp8(C.byref(s), _p(src), int(rows), _p(n_rows), _p(q), _p(qs),
+                                   _stream(stream)))
+
+
+def moe_quant_weights_fp8(s, W_gu, W_down, w: Fp8Weights, stream=None):
+    fn, d, F, E_l = "moe_quant_weights_fp8", s.d, s.F, s.E_l
+    _chk(s, fn, "W_gu", W_gu, _DATA, E_l * 2 * F * d)
+    _chk(s, fn, "W_down", W_down, _DATA, E_l * d * F)
+    check(lib().moe_quant_weights_fp8(C.byref(s), _p(W_gu), _p(W_down), w.check(fn, s),
+                                      _stream(stream)))
+
+
+def _chk_fp8(s, fn, q, qs, pair_of_row, offsets, tile_offsets, ws):
+    rows = s.T * s.K if pair_of_row is None else s.T
+    _chk(s, fn, "quantised rows", q, _FP8, rows * s.d)
+    _chk(s, fn, "row scales", qs, _U8, rows * ((s.d // MOE_FP8_BLOCK + 3) // 4 * 4))
+    _chk(s, fn, "pair_of_row", pair_of_row, _I32, s.T * s.K, optional=True)
+    _chk(s, fn, "offsets", offsets, _I32, s.E_l + 1)
+    _chk(s, fn, "tile_offsets", tile_offsets, _I32, s.E_l + 1)
+    _chk_ws(fn, ws)
+
+
+def moe_expert_ffn_fwd_fp8(s, xq, xs, pair_of_row, offsets, tile_offsets, w: Fp8Weights, h, a, yp,
+                           ws, stream=None):
+    """pair_of_row None: xq, xs hold the dispatched rows; else the tokens.  h and
+    a may be None (not written)."""
+    fn, cap, d, F = "moe_expert_ffn_fwd_fp8", s.T * s.K, s.d, s.F
+    _chk_fp8(s, fn, xq, xs, pair_of_row, offsets, tile_offsets, ws)
+    _chk(s, fn, "h", h, _DATA, cap * 2 * F, optional=True)
+    _chk(s, fn, "a", a, _DATA, cap * F, optional=True)
+    _chk(s, fn, "yp", yp, _DATA, cap * d)
+    wp, wb = _ws(ws)
+    check(lib().moe_expert_ffn_fwd_fp8(C.byref(s), _p(xq), _p(xs), _p(pair_of_row), _p(offsets),
+                                       _p(tile_offsets), w.check(fn, s), _p(h), _p(a), _p(yp),
+                                       wp, wb, _stream(stream)))
+
+
+def moe_ffn_dgrad_fp8(s, dq, ds, pair_of_row, gates, h, offsets, tile_offsets, w: Fp8Weights, dh,
+                      dxp, ag, ws, stream=None):
+    """pair_of_row None: dq, ds hold the quantised dyp by dispatched row (gates and
+    ag None); else the quantised dout by token, with the pairs' gates."""
+    fn, cap, d, F = "moe_ffn_dgrad_fp8", s.T * s.K, s.d, s.F
+    _chk_fp8(s, fn, dq, ds, pair_of_row, offsets, tile_offsets, ws)
+    _chk(s, fn, "gates", gates, _F32, cap, optional=True)
+    _chk(s, fn, "h", h, _DATA, cap * 2 * F)
+    _chk(s, fn, "dh", dh, _DATA, cap * 2 * F)
+    _chk(s, fn, "dxp", dxp, _DATA, cap * d)
+    _chk(s, fn, "ag", ag, _DATA, cap * F, optional=True)
+    wp, wb = _ws(ws)
+    check(lib().moe_ffn_dgrad_fp8(C.byref(s), _p(dq), _p(ds), _p(pair_of_row), _p(gates), _p(h),
+                                  _p(offsets), _p(tile_offsets), w.check(fn, s), _p(dh), _p(dxp),
+                                  _p(ag), wp, wb, _stream(stream)))
+
+
+# ---- weight update ----------------------------------------------------------
+class AdamWTensors:
+    """The tensors of an AdamW step, checked once and kept for many steps.  Each
+    is a dict: param (float32, bfloat16 or float16), grad (float32), m and v
+    (float32, or float8_e4m3fn with uint8 scales m_s and v_s of
+    ceil(n / 128) elements), and optionally master (float32) and weight_decay."""
+
+    def __init__(self, tensors):
+        import torch
+
+        fn = "AdamWTensors"
+        dts = {torch.float32: MOE_F32, torch.bfloat16: MOE_BF16, torch.float16: MOE_F16}
+        self.tensors = [dict(t) for t in tensors]
+        self.array = (MoeAdamwTensor * max(1, len(self.tensors)))()
+        for i, t in enumerate(self.tensors):
+            p = t["param"]
+            if not isinstance(p, torch.Tensor) or p.dtype not in dts:
+                raise MoeError(MOE_ERR_DTYPE, f"{fn}: param {i} must be a float32, bfloat16 or "
+                                              "float16 tensor")
+            n, q8 = p.numel(), t["m"].dtype == torch.float8_e4m3fn
+            s = MoeShape(dtype=dts[p.dtype])
+            nb = -(-n // MOE_FP8_BLOCK)
+            for name, kind, want, opt in (
+                    ("param", _DATA, n, False), ("grad", _F32, n, False),
+                    ("master", _F32, n, True), ("m", _FP8 if q8 else _F32, n, False),
+                    ("v", _FP8 if q8 else _F32, n, False), ("m_s", _U8, nb, not q8),
+                    ("v_s", _U8, nb, not q8)):
+                x = t.get(name)
+                _chk(s, fn, f"{name} {i}", x, kind, want, optional=opt)
+                if x is not None and (x.numel() != want or x.device != p.device):
+                    raise MoeError(MOE_ERR_ARG, f"{fn}: {name} {i} has {x.numel()} elements on "
+                                                f"{x.device}, needs {want} on {p.device}")
+            self.array[i] = MoeAdamwTensor(
+                n, *[_p(t.get(k)) for k in ("param", "master", "grad", "m", "v", "m_s", "v_s")],
+                s.dtype, int(q8), float(t.get("weight_decay", 0.0)), 0)
+
+
+def moe_adamw(tensors, lr, beta1=0.9, beta2=0.999, eps=1e-8, step=1, grad_scale=1.0,
+              grad_scale_dev=None, seed=0, stream=None):
+    """tensors: an AdamWTensors (or the list of dicts to make one of)."""
+    if not isinstance(tensors, AdamWTensors):
+        tensors = AdamWTensors(tensors)
+    _chk(MoeShape(dtype=MOE_F32), "moe_adamw", "grad_scale_dev", grad_scale_dev, _F32, 1,
+         optional=True)
+    hp = MoeAdamwHyper(lr, beta1, beta2, eps, int(step), int(seed) & (2 ** 64 - 1),
+                       _p(grad_scale_dev), grad_scale, 0)
+    check(lib().moe_adamw(tensors.array, len(tensors.tensors), C.byref(hp), _stream(stream)))
 
 
 def moe_overlap_step(step: MoeStep, s_compute=None, s_copy=None, flags=0):

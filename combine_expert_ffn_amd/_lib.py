@@ -71,8 +71,32 @@ class MoeStep(C.Structure):
                 ("dW_gu_s", C.c_void_p), ("dW_down_s", C.c_void_p)]
 
 
+MOE_FP8_BLOCK = 128
+
+FP8_WEIGHT_FIELDS = ["gu", "gu_s", "down", "down_s", "guT", "guT_s", "downT", "downT_s"]
+
+
+class MoeFp8Weights(C.Structure):
+    _fields_ = [(n, C.c_void_p) for n in FP8_WEIGHT_FIELDS]
+
+
+class MoeAdamwTensor(C.Structure):
+    _fields_ = [("n", C.c_int64)] + [(n, C.c_void_p) for n in ("param", "master", "grad", "m", "v",
+                                                               "m_s", "v_s")] + [
+        ("dtype", C.c_int32), ("state8", C.c_int32), ("weight_decay", C.c_float),
+        ("reserved", C.c_int32)]
+
+
+class MoeAdamwHyper(C.Structure):
+    _fields_ = [("lr", C.c_double), ("beta1", C.c_double), ("beta2", C.c_double),
+                ("eps", C.c_double), ("step", C.c_int64), ("seed", C.c_uint64),
+                ("grad_scale_dev", C.c_void_p), ("grad_scale", C.c_float),
+                ("reserved", C.c_int32)]
+
+
 _P = C.c_void_p
 _SP = C.POINTER(MoeShape)
+_WP = C.POINTER(MoeFp8Weights)
 SIGNATURES = {
     "moe_workspace_bytes": (C.c_size_t, [_SP]),
     "moe_step_workspace_bytes": (C.c_size_t, [_SP]),
@@ -111,6 +135,15 @@ SIGNATURES = {
     "moe_route_bwd": (C.c_int, [_SP, C.c_int, _P, _P, _P, _P, _P, _P, C.c_int, _P, C.c_size_t,
                                 _P]),
     "moe_dispatch_bwd": (C.c_int, [_SP, _P, _P, _P, _P, _P, _P, C.c_int, _P, C.c_size_t, _P]),
+    "moe_fp8_scale_ld": (C.c_int64, [C.c_int64]),
+    "moe_fp8_workspace_bytes": (C.c_size_t, [_SP]),
+    "moe_quant_rows_fp8": (C.c_int, [_SP, _P, C.c_int64, _P, _P, _P, _P]),
+    "moe_quant_weights_fp8": (C.c_int, [_SP, _P, _P, _WP, _P]),
+    "moe_expert_ffn_fwd_fp8": (C.c_int, [_SP, _P, _P, _P, _P, _P, _WP, _P, _P, _P, _P, C.c_size_t,
+                                         _P]),
+    "moe_ffn_dgrad_fp8": (C.c_int, [_SP, _P, _P, _P, _P, _P, _P, _P, _WP, _P, _P, _P, _P,
+                                    C.c_size_t, _P]),
+    "moe_adamw": (C.c_int, [C.POINTER(MoeAdamwTensor), C.c_int, C.POINTER(MoeAdamwHyper), _P]),
     "moe_overlap_step": (C.c_int, [C.POINTER(MoeStep), _P, _P, C.c_int]),
     "moe_overlap_steps": (C.c_int, [C.POINTER(MoeStep), C.c_int, _P, _P, C.c_int]),
     "moe_timing_enable": (C.c_int, [C.c_int]),

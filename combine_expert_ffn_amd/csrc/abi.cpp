@@ -2,6 +2,7 @@
 // two-micro-batch step.  Every entry point validates all of its arguments
 // before the first launch, so a rejected call writes nothing.
 #include "moe_internal.h"
+#include "moe_fp8.h"
 
 #include <dlfcn.h>
 #include <stdarg.h>
@@ -98,7 +99,7 @@ void KernelTimer::stop() {
   slot = -1;
 }
 
-static int validate_shape(const moe_shape* s) {
+int validate_shape(const moe_shape* s) {
   if (!s) return set_error(MOE_ERR_NULL, "shape is NULL");
   if (s->dtype != MOE_F32 && s->dtype != MOE_BF16 && s->dtype != MOE_F16)
     return set_error(MOE_ERR_DTYPE, "dtype %d is not MOE_F32, MOE_BF16 or MOE_F16", s->dtype);

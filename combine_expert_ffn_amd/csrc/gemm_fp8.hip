@@ -1,0 +1,582 @@
+// Grouped expert products on 8-bit operands (gfx950): e4m3 values with a
+// power-of-two scale per 128 along the reduction, float32 accumulation
+// (v_mfma_scale_f32_32x32x64_f8f6f4).  The instruction multiplies each lane's
+// 32 values by a scale byte of that lane's own, so the block scales of both
+// operands enter without a vector instruction and every block's products go
+// into the one accumulator.
+//
+// A stage of the reduction is one block of 128 values = 128 bytes per row, the
+// bytes of 64 values in 16 bits, and a 32 x 32 x 64 instruction takes 64 cycles
+// for 64 bytes of each row as the 16-bit one takes 32 for 32: the tile that
+// balances LDS reads against the matrix cores there does so here.
+//  * block tile 256 x 256, 8 waves (2 per SIMD) of 64 x 128 = 2 x 4 MFMA tiles;
+//    a wave's 128 columns are whole scale blocks of the output, so the fused
+//    quantisation needs at most one exchange with another wave;
+//  * two LDS stages of [rows][128 bytes], the 16-byte chunk index XOR-swizzled
+//    by the row; a lane's 32 bytes are the chunks 2t + lane / 32 of two
+//    consecutive pairs t, the same for both operands (the order of the values
+//    within a block does not change its sum);
+//  * persistent grid over the dispatch plan's row tiles, one range per XCD.
+#include "moe_fp8.h"
+
+namespace moe {
+namespace {
+
+typedef int i32x4_t __attribute__((ext_vector_type(4)));
+typedef int i32x8_t __attribute__((ext_vector_type(8)));
+typedef unsigned int u32x4_t __attribute__((ext_vector_type(4)));
+typedef float f32x16_t __attribute__((ext_vector_type(16)));
+
+struct BF16 { typedef uint16_t elt; };
+struct F16 { typedef _Float16 elt; };
+
+constexpr int BM = 256, BN = 256, NT = 512;
+constexpr int WGN = 2;                    // waves along N; 4 along M
+constexpr int WTM = 64, WTN = 128;        // wave tile
+constexpr int TM = WTM / 32, TN = WTN / 32;
+constexpr int STAGE = BM * 128;           // bytes of one operand's stage
+static_assert(BM == kTileM, "row tiles come from the dispatch plan");
+// Epilogue staging: 32 rows x 128 columns of floats per wave, rows 132 apart.
+constexpr int EP_LD = 132;
+constexpr int SMEM = NT / 64 * 32 * EP_LD * 4;
+static_assert(SMEM >= 4 * STAGE, "the stages fit the epilogue's LDS");
+
+__device__ __forceinline__ int swz(int row) { return (row & 7) ^ ((row >> 3) & 1); }
+
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc_of(const void* p) {
+  // raw buffer (stride 0); every offset used is a valid byte of the operand
+  return __builtin_amdgcn_make_buffer_rsrc((void*)p, (short)0, 0x7fffffff, 0x00020000);
+}
+
+// One operand's 256 rows: 4 chunks of 16 bytes per thread and stage, chunk c
+// at tile row c * 64 + tid / 8, 16-byte chunk tid % 8.
+struct Load {
+  u32x4_t v[4];
+  __amdgpu_buffer_rsrc_t rsrc;
+  uint32_t off[4];
+  int dst0;
+  template <class RowOff>
+  __device__ __forceinline__ void init(const void* base, RowOff row_off, int tid) {
+    rsrc = rsrc_of(base);
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+      off[c] = (uint32_t)row_off(c * 64 + (tid >> 3)) + (uint32_t)(tid & 7) * 16u;
+    const int row = tid >> 3;  // rows 64 apart have the same swizzle
+    dst0 = row * 128 + (((tid & 7) ^ swz(row)) << 4);
+  }
+  __device__ __forceinline__ void load(int kt) {
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+      v[c] = __builtin_amdgcn_raw_buffer_load_b128(rsrc, (int)off[c], kt * 128, 0);
+  }
+  __device__ __forceinline__ void store(uint8_t* lds) const {
+#pragma unroll
+    for (int c = 0; c < 4; ++c) *(u32x4_t*)(lds + dst0 + c * 64 * 128) = v[c];
+  }
+};
+
+// Scale bytes of four stages at a time: of the wave's rows (one per lane and
+// 32-row tile) and of the two 64-column halves of its columns.
+struct Scales {
+  __amdgpu_buffer_rsrc_t ra, rb;
+  uint32_t oa[TM], ob[2];
+  uint32_t a[TM], b[2], an[TM], bn[2];
+  __device__ __forceinline__ void fetch(int kt) {
+#pragma unroll
+    for (int i = 0; i < TM; ++i) an[i] = __builtin_amdgcn_raw_buffer_load_b32(ra, (int)oa[i], kt, 0);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) bn[h] = __builtin_amdgcn_raw_buffer_load_b32(rb, (int)ob[h], kt, 0);
+  }
+  __device__ __forceinline__ void next() {
+#pragma unroll
+    for (int i = 0; i < TM; ++i) a[i] = an[i];
+    b[0] = bn[0];
+    b[1] = bn[1];
+  }
+};
+
+__device__ __forceinline__ i32x8_t read_frag(const uint8_t* tile, int row0, int kk, int lane) {
+  const int fr = lane & 31, hf = lane >> 5;
+  const uint8_t* p = tile + (row0 + fr) * 128;
+  const int s = swz(fr);
+  const i32x4_t lo = *(const i32x4_t*)(p + (((kk * 4 + hf) ^ s) << 4));
+  const i32x4_t hi = *(const i32x4_t*)(p + (((kk * 4 + 2 + hf) ^ s) << 4));
+  return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+}
+
+// Wave and lane index next to their use (the lane index opaque to the optimiser,
+// so that addresses made from it are not held across the main loop).
+struct Pos {
+  int lane, wave, wm, wn;
+  static __device__ __forceinline__ Pos of() {
+    const int w = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+    int l = (int)__builtin_amdgcn_mbcnt_hi(~0u, __builtin_amdgcn_mbcnt_lo(~0u, 0u));
+    asm volatile("" : "+v"(l));
+    return {l, w, w / WGN, w % WGN};
+  }
+};
+
+// The reduction over nk stages, once stage 0 is in LDS buffer 0 and stage 1 in
+// the loaders' registers.  Ends with a barrier: the LDS is free.
+__device__ __forceinline__ void mainloop(Load& la, Load& lb, Scales& sc, int nk, uint8_t* smem,
+                                         f32x16_t (&acc)[TM][TN]) {
+  const Pos w = Pos::of();
+#pragma unroll
+  for (int i = 0; i < TM; ++i)
+#pragma unroll
+    for (int j = 0; j < TN; ++j)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.f;
+  for (int kt = 0; kt < nk; ++kt) {
+    uint8_t* cur = smem + (kt & 1) * 2 * STAGE;
+    uint8_t* nxt = smem + (~kt & 1) * 2 * STAGE;
+    if ((kt & 3) == 0) {
+      sc.next();
+      sc.fetch(min(kt + 4, (nk - 1) & ~3));
+    }
+    const int sh = (kt & 3) * 8;
+    uint32_t sa[TM], sb[2];
+#pragma unroll
+    for (int i = 0; i < TM; ++i) sa[i] = sc.a[i] >> sh;
+    sb[0] = sc.b[0] >> sh;
+    sb[1] = sc.b[1] >> sh;
+    la.store(nxt);
+    lb.store(nxt + STAGE);
+    const int k2 = min(kt + 2, nk - 1);
+    la.load(k2);
+    lb.load(k2);
+#pragma unroll
+    for (int kk = 0; kk < 2; ++kk) {
+      i32x8_t a[TM], b[TN];
+#pragma unroll
+      for (int i = 0; i < TM; ++i) a[i] = read_frag(cur, w.wm * WTM + i * 32, kk, w.lane);
+#pragma unroll
+      for (int j = 0; j < TN; ++j) b[j] = read_frag(cur + STAGE, w.wn * WTN + j * 32, kk, w.lane);
+#pragma unroll
+      for (int j = 0; j < TN; ++j)
+#pragma unroll
+        for (int i = 0; i < TM; ++i)
+          acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
+              a[i], b[j], acc[i][j], 0, 0, 0, (int)sa[i], 0, (int)sb[j >> 1]);
+    }
+    __syncthreads();
+  }
+}
+
+// Persistent schedule: the blocks form G = min(8, grid) groups by block % G
+// (with G = 8 a group is one XCD); group g owns tiles [g*total/G, (g+1)*total/G),
+// handed out to its blocks round robin.
+struct Sched {
+  int t, end, step;
+  __device__ __forceinline__ explicit Sched(int total) {
+    const int nb = gridDim.x, G = nb < 8 ? nb : 8;
+    const int g = blockIdx.x % G, slot = blockIdx.x / G;
+    t = (int)((long)total * g / G) + slot;
+    end = (int)((long)total * (g + 1) / G);
+    step = (nb - g + G - 1) / G;
+  }
+};
+
+// (expert, first row, row end) of M-tile mt from LDS copies of the plan, in
+// scalar registers.
+__device__ __forceinline__ void row_tile(const int* s_to, const int* s_off, int E_l, int mt,
+                                         int& e, int& m0, int& m_end) {
+  int lo = 0, hi = E_l;  // s_to[lo] <= mt < s_to[hi]
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (s_to[mid] <= mt) lo = mid;
+    else hi = mid;
+  }
+  e = __builtin_amdgcn_readfirstlane(lo);
+  m0 = __builtin_amdgcn_readfirstlane(s_off[lo] + (mt - s_to[lo]) * kTileM);
+  m_end = __builtin_amdgcn_readfirstlane(s_off[lo + 1]);
+}
+
+// The row operand of a product: rows of the dispatched matrix, or token rows
+// gathered through the plan.
+struct Rows {
+  const uint8_t* q;
+  const uint8_t* s;
+  int k, ld;              // bytes per row, scale bytes per row
+  const int32_t* xrows;   // NULL: dispatched rows
+  int K;
+  __device__ __forceinline__ void init(int m0, int m_end, Load& la, Scales& sc, int tid) const {
+    const Pos w = Pos::of();
+    const int sr = w.wm * WTM + (w.lane & 31);
+    if (xrows) {  // block-uniform
+      la.init(q, [&](int r) { return xrows[min(m0 + r, m_end - 1)] / K * k; }, tid);
+      sc.ra = rsrc_of(s);
+#pragma unroll
+      for (int i = 0; i < TM; ++i)
+        sc.oa[i] = (uint32_t)(xrows[min(m0 + sr + i * 32, m_end - 1)] / K) * (uint32_t)ld;
+    } else {
+      la.init(q + (size_t)m0 * k, [&](int r) { return (min(m0 + r, m_end - 1) - m0) * k; }, tid);
+      sc.ra = rsrc_of(s + (size_t)m0 * ld);
+#pragma unroll
+      for (int i = 0; i < TM; ++i)
+        sc.oa[i] = (uint32_t)(min(m0 + sr + i * 32, m_end - 1) - m0) * (uint32_t)ld;
+    }
+  }
+};
+
+// The weight operand [E_l][n][k] with scales [E_l][n / 128][ld].
+struct Cols {
+  const uint8_t* q;
+  const uint8_t* s;
+  int n, k, ld;
+  // plain columns nt * 256 + ..., clamped to the matrix
+  __device__ __forceinline__ void init(int e, int nt, Load& lb, Scales& sc, int tid) const {
+    const Pos w = Pos::of();
+    lb.init(q + (size_t)e * n * k, [&](int c) { return min(nt * BN + c, n - 1) * k; }, tid);
+    sc.rb = rsrc_of(s + (size_t)e * (n / 128) * ld);
+    sc.ob[0] = sc.ob[1] = (uint32_t)(min(nt * 2 + w.wn, n / 128 - 1) * ld);
+  }
+};
+
+// Accumulator tile i of this wave as 32 rows x 128 columns in the wave's own LDS
+// area (operations of one wave on LDS complete in order).
+__device__ __forceinline__ const float* stage_rows(const f32x16_t (&acc)[TM][TN], int i,
+                                                   uint8_t* smem, const Pos& w) {
+  float* reg = reinterpret_cast<float*>(smem) + w.wave * 32 * EP_LD;
+#pragma unroll
+  for (int j = 0; j < TN; ++j)
+#pragma unroll
+    for (int r = 0; r < 16; ++r)
+      reg[(8 * (r >> 2) + 4 * (w.lane >> 5) + (r & 3)) * EP_LD + j * 32 + (w.lane & 31)] =
+          acc[i][j][r];
+  return reg;
+}
+__device__ __forceinline__ void ld8(const float* p, float* f) {
+  const float4 a = *(const float4*)p, b = *(const float4*)(p + 4);
+  f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
+  f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
+}
+__device__ __forceinline__ float amax8(const float* f) {
+  float m = 0.f;
+#pragma unroll
+  for (int t = 0; t < 8; ++t) m = fmaxf(m, finite_abs(f[t]));
+  return m;
+}
+__device__ __forceinline__ uint2 quant8(const float* f, float inv) {
+  float y[8];
+#pragma unroll
+  for (int t = 0; t < 8; ++t) y[t] = finite_or_nan(f[t]) * inv;
+  return uint2{pack_fp8(y[0], y[1], y[2], y[3]), pack_fp8(y[4], y[5], y[6], y[7])};
+}
+// Largest value over rows of 8 or 16 lanes.
+template <int N>
+__device__ __forceinline__ float lanes_max(float v) {
+  auto step = [](float x, int moved) { return fmaxf(x, __int_as_float(moved)); };
+  v = step(v, __builtin_amdgcn_update_dpp(0, __float_as_int(v), 0xB1, 0xF, 0xF, true));
+  v = step(v, __builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x4E, 0xF, 0xF, true));
+  v = step(v, __builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x141, 0xF, 0xF, true));
+  if constexpr (N == 16)
+    v = step(v, __builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x140, 0xF, 0xF, true));
+  return v;
+}
+
+// forward GEMM1: [g, u] = x^ . W_gu^[e]^T, a = silu(g) u, quantised for GEMM2.
+// A tile is 128 outputs: the 128 tile columns of wave column wn are 64 gate
+// rows and the 64 up rows of the same outputs.  The tile's outputs are one
+// scale block per row; its two halves' largest magnitudes meet in LDS.
+template <class E>
+struct GateUpOp {
+  typedef typename E::elt elt;
+  Rows x;
+  Cols w;  // n = 2F
+  elt *h, *a;
+  uint8_t *aq, *as;
+  int F, ldF;
+  __device__ __forceinline__ int stages() const { return x.k / 128; }
+  __device__ __forceinline__ void init(int e, int m0, int m_end, int nt, Load& la, Load& lb,
+                                       Scales& sc, int tid) const {
+    x.init(m0, m_end, la, sc, tid);
+    lb.init(w.q + (size_t)e * w.n * w.k, [&](int c) {
+      const int j = nt * 128 + (c >> 7) * 64 + (c & 63);
+      return (((c >> 6) & 1) * F + j) * w.k;
+    }, tid);
+    sc.rb = rsrc_of(w.s + (size_t)e * (w.n / 128) * w.ld);
+    sc.ob[0] = (uint32_t)(nt * w.ld);
+    sc.ob[1] = (uint32_t)((F / 128 + nt) * w.ld);
+  }
+  __device__ __forceinline__ void epilogue(const f32x16_t (&acc)[TM][TN], int m0, int m_end,
+                                           int nt, uint8_t* smem, float* s_max) const {
+    const Pos p = Pos::of();
+    const int c = (p.lane & 7) * 8, j0 = nt * 128 + p.wn * 64 + c;
+    float av[TM][4][8];
+#pragma unroll
+    for (int i = 0; i < TM; ++i) {
+      const float* blk = stage_rows(acc, i, smem, p);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int r = q * 8 + (p.lane >> 3), tr = p.wm * WTM + i * 32 + r;
+        float g[8], u[8];
+        ld8(blk + r * EP_LD + c, g);
+        ld8(blk + r * EP_LD + 64 + c, u);
+#pragma unroll
+        for (int t = 0; t < 8; ++t) av[i][q][t] = silu_fast(g[t]) * u[t];
+        const float mx = lanes_max<8>(amax8(av[i][q]));
+        if ((p.lane & 7) == 0) s_max[p.wn * BM + tr] = mx;
+        if (m0 + tr < m_end) {
+          const size_t row = (size_t)(m0 + tr);
+          if (h) {
+            *(uint4*)(h + row * 2 * F + j0) = Chunk<elt>::pack(g);
+            *(uint4*)(h + row * 2 * F + F + j0) = Chunk<elt>::pack(u);
+          }
+          if (a) *(uint4*)(a + row * F + j0) = Chunk<elt>::pack(av[i][q]);
+        }
+      }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < TM; ++i)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int tr = p.wm * WTM + i * 32 + q * 8 + (p.lane >> 3);
+        const int byte = fp8_scale_byte(fmaxf(s_max[tr], s_max[BM + tr]));
+        if (m0 + tr < m_end) {
+          const size_t row = (size_t)(m0 + tr);
+          *(uint2*)(aq + row * F + j0) = quant8(av[i][q], fp8_inv_scale(byte));
+          if (p.wn == 0 && (p.lane & 7) == 0) as[row * ldF + nt] = (uint8_t)byte;
+        }
+      }
+  }
+};
+
+// Products whose result is stored as it is: forward GEMM2 (y_p = a^ . W_down^T) and
+// the second of the dgrad (dx_p = dh^ . W_gu, with the transposed weights).
+template <class E>
+struct PlainOp {
+  typedef typename E::elt elt;
+  Rows x;
+  Cols w;
+  elt* out;  // [rows][w.n]
+  __device__ __forceinline__ int stages() const { return x.k / 128; }
+  __device__ __forceinline__ void init(int e, int m0, int m_end, int nt, Load& la, Load& lb,
+                                       Scales& sc, int tid) const {
+    x.init(m0, m_end, la, sc, tid);
+    w.init(e, nt, lb, sc, tid);
+  }
+  __device__ __forceinline__ void epilogue(const f32x16_t (&acc)[TM][TN], int m0, int m_end,
+                                           int nt, uint8_t* smem, float*) const {
+    const Pos p = Pos::of();
+    const int cb = nt * BN + p.wn * WTN, c = (p.lane & 15) * 8;
+    if (cb >= w.n) return;  // wave-uniform; n is a multiple of 128
+#pragma unroll
+    for (int i = 0; i < TM; ++i) {
+      const float* blk = stage_rows(acc, i, smem, p);
+#pragma unroll
+      for (int q = 0; q < 8; ++q) {
+        const int r = q * 4 + (p.lane >> 4), row = m0 + p.wm * WTM + i * 32 + r;
+        float f[8];
+        ld8(blk + r * EP_LD + c, f);
+        if (row < m_end) *(uint4*)(out + (size_t)row * w.n + cb + c) = Chunk<elt>::pack(f);
+      }
+    }
+  }
+};
+
+// dgrad GEMM A: da = [gate] d^ . W_down^[e] with the SwiGLU backward; dg and du of a
+// wave's 128 columns are one scale block each.
+template <class E>
+struct DgradActOp {
+  typedef typename E::elt elt;
+  Rows x;
+  Cols w;  // W_down transposed, n = F
+  const elt* h;
+  const float* gates;  // with x.xrows
+  elt *dh, *ag;
+  uint8_t *dq, *ds;  // [rows][2F], [rows][ld2F]
+  int F, ld2F;
+  __device__ __forceinline__ int stages() const { return x.k / 128; }
+  __device__ __forceinline__ void init(int e, int m0, int m_end, int nt, Load& la, Load& lb,
+                                       Scales& sc, int tid) const {
+    x.init(m0, m_end, la, sc, tid);
+    w.init(e, nt, lb, sc, tid);
+  }
+  __device__ __forceinline__ void epilogue(const f32x16_t (&acc)[TM][TN], int m0, int m_end,
+                                           int nt, uint8_t* smem, float*) const {
+    const Pos p = Pos::of();
+    const int cb = nt * BN + p.wn * WTN, c = (p.lane & 15) * 8;
+    if (cb >= F) return;  // wave-uniform; F is a multiple of 128
+#pragma unroll
+    for (int i = 0; i < TM; ++i) {
+      const float* blk = stage_rows(acc, i, smem, p);
+#pragma unroll
+      for (int q = 0; q < 8; ++q) {
+        const int r = q * 4 + (p.lane >> 4), rr = m0 + p.wm * WTM + i * 32 + r;
+        const size_t row = (size_t)min(rr, m_end - 1);
+        float da[8], g[8], u[8], dg[8], du[8], av[8];
+        ld8(blk + r * EP_LD + c, da);
+        Chunk<elt>::unpack(*(const uint4*)(h + row * 2 * F + cb + c), g);
+        Chunk<elt>::unpack(*(const uint4*)(h + row * 2 * F + F + cb + c), u);
+        const float gate = x.xrows ? gates[x.xrows[row]] : 1.f;
+#pragma unroll
+        for (int t = 0; t < 8; ++t) {
+          const float sg = sigmoid_fast(g[t]), d = da[t] * gate;
+          dg[t] = d * u[t] * sg * (1.0f + g[t] * (1.0f - sg));
+          du[t] = d * g[t] * sg;
+          av[t] = gate * (g[t] * sg) * u[t];
+        }
+        const int bg = fp8_scale_byte(lanes_max<16>(amax8(dg)));
+        const int bu = fp8_scale_byte(lanes_max<16>(amax8(du)));
+        if (rr < m_end) {
+          *(uint4*)(dh + row * 2 * F + cb + c) = Chunk<elt>::pack(dg);
+          *(uint4*)(dh + row * 2 * F + F + cb + c) = Chunk<elt>::pack(du);
+          if (ag) *(uint4*)(ag + row * F + cb + c) = Chunk<elt>::pack(av);
+          *(uint2*)(dq + row * 2 * F + cb + c) = quant8(dg, fp8_inv_scale(bg));
+          *(uint2*)(dq + row * 2 * F + F + cb + c) = quant8(du, fp8_inv_scale(bu));
+          if ((p.lane & 15) == 0) {
+            ds[row * ld2F + cb / 128] = (uint8_t)bg;
+            ds[row * ld2F + (F + cb) / 128] = (uint8_t)bu;
+          }
+        }
+      }
+    }
+  }
+};
+
+// Row-grouped product over the plan's tiles.  The first stage of the next tile is
+// loaded before the epilogue issues its stores (memory operations of a wave
+// complete in order, so the next main loop need not wait for them).
+template <class Op>
+__global__ __launch_bounds__(NT) void fp8_kernel(Op op, const int32_t* __restrict__ offsets,
+                                                 const int32_t* __restrict__ tile_offsets,
+                                                 int E_l, int n_tiles) {
+  __shared__ __attribute__((aligned(16))) uint8_t smem[SMEM];
+  __shared__ float s_max[2 * BM];
+  __shared__ int s_to[257], s_off[257];
+  for (int j = threadIdx.x; j <= E_l; j += NT) {
+    s_to[j] = tile_offsets[j];
+    s_off[j] = offsets[j];
+  }
+  __syncthreads();
+  Sched sch(s_to[E_l] * n_tiles);
+  if (sch.t >= sch.end) return;  // block-uniform
+  const int tid = threadIdx.x, nk = op.stages(), k1 = nk > 1 ? 1 : 0;
+  Load la, lb;
+  Scales sc;
+  int e, m0, m_end, nt = sch.t % n_tiles;
+  row_tile(s_to, s_off, E_l, sch.t / n_tiles, e, m0, m_end);
+  op.init(e, m0, m_end, nt, la, lb, sc, tid);
+  sc.fetch(0);
+  la.load(0);
+  lb.load(0);
+  for (;;) {
+    la.store(smem);
+    lb.store(smem + STAGE);
+    la.load(k1);
+    lb.load(k1);
+    __syncthreads();
+    f32x16_t acc[TM][TN];
+    mainloop(la, lb, sc, nk, smem, acc);
+    const int cm0 = m0, cm_end = m_end, cnt = nt;
+    sch.t += sch.step;
+    const bool more = sch.t < sch.end;  // block-uniform
+    if (more) {
+      nt = sch.t % n_tiles;
+      row_tile(s_to, s_off, E_l, sch.t / n_tiles, e, m0, m_end);
+      op.init(e, m0, m_end, nt, la, lb, sc, tid);
+      sc.fetch(0);
+      la.load(0);
+      lb.load(0);
+    }
+    op.epilogue(acc, cm0, cm_end, cnt, smem, s_max);
+    __syncthreads();  // the staging is read before the next tile's stage 0 lands in LDS
+    if (!more) break;
+  }
+}
+
+inline int max_row_tiles(const moe_shape* s) {
+  return (int)((s->T * s->K + s->E_l * (int64_t)(kTileM - 1)) / kTileM);
+}
+
+// One block per CU of the current device (at most `tiles`).
+inline int persistent_grid(long tiles) {
+  int dev = 0, n = 0;
+  if (hipGetDevice(&dev) != hipSuccess ||
+      hipDeviceGetAttribute(&n, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess || n <= 0)
+    n = 256;
+  return (int)(tiles < n ? (tiles > 0 ? tiles : 1) : n);
+}
+
+template <class Op>
+int launch(const char* name, const moe_shape* s, const Op& op, const int32_t* offsets,
+           const int32_t* tile_offsets, int n_tiles, hipStream_t st) {
+  const int grid = persistent_grid((long)max_row_tiles(s) * n_tiles);
+  MOE_LAUNCH(name, st, fp8_kernel<Op><<<grid, NT, 0, st>>>(op, offsets, tile_offsets, (int)s->E_l,
+                                                           n_tiles));
+  return check_launch(name);
+}
+
+struct Ws {
+  uint8_t *q, *s;
+  Ws(const moe_shape* sh, void* ws, int64_t cols)
+      : q((uint8_t*)ws), s(q + align_up((size_t)(sh->T * sh->K * cols), 256)) {}
+};
+
+template <class E>
+int ffn_fwd_t(const moe_shape* s, const void* xq, const uint8_t* xs, const int32_t* xrows,
+              const int32_t* offsets, const int32_t* tile_offsets, const moe_fp8_weights* w,
+              void* h, void* a, void* yp, void* ws, hipStream_t st) {
+  typedef typename E::elt elt;
+  const int d = (int)s->d, F = (int)s->F, K = (int)s->K;
+  const int ld_d = (int)fp8_scale_ld(d), ld_f = (int)fp8_scale_ld(F);
+  const Ws q(s, ws, F);
+  const GateUpOp<E> gu{{(const uint8_t*)xq, xs, d, ld_d, xrows, K},
+                       {(const uint8_t*)w->gu, w->gu_s, 2 * F, d, ld_d},
+                       (elt*)h, (elt*)a, q.q, q.s, F, ld_f};
+  if (int rc = launch("ffn_gate_up_fp8", s, gu, offsets, tile_offsets, F / 128, st)) return rc;
+  const PlainOp<E> dn{{q.q, q.s, F, ld_f, nullptr, K},
+                      {(const uint8_t*)w->down, w->down_s, d, F, ld_f}, (elt*)yp};
+  return launch("ffn_down_fp8", s, dn, offsets, tile_offsets, (d + BN - 1) / BN, st);
+}
+
+template <class E>
+int ffn_dgrad_t(const moe_shape* s, const void* dq, const uint8_t* ds, const int32_t* xrows,
+                const float* gates, const void* h, const int32_t* offsets,
+                const int32_t* tile_offsets, const moe_fp8_weights* w, void* dh, void* dxp,
+                void* ag, void* ws, hipStream_t st) {
+  typedef typename E::elt elt;
+  const int d = (int)s->d, F = (int)s->F, K = (int)s->K;
+  const int ld_d = (int)fp8_scale_ld(d), ld_2f = (int)fp8_scale_ld(2 * F);
+  const Ws q(s, ws, 2 * F);
+  const DgradActOp<E> act{{(const uint8_t*)dq, ds, d, ld_d, xrows, K},
+                          {(const uint8_t*)w->downT, w->downT_s, F, d, ld_d},
+                          (const elt*)h, gates, (elt*)dh, (elt*)ag, q.q, q.s, F, ld_2f};
+  if (int rc = launch("dgrad_act_fp8", s, act, offsets, tile_offsets, (F + BN - 1) / BN, st))
+    return rc;
+  const PlainOp<E> in{{q.q, q.s, 2 * F, ld_2f, nullptr, K},
+                      {(const uint8_t*)w->guT, w->guT_s, d, 2 * F, ld_2f}, (elt*)dxp};
+  return launch("dgrad_in_fp8", s, in, offsets, tile_offsets, (d + BN - 1) / BN, st);
+}
+
+}  // namespace
+
+size_t fp8_workspace_bytes(const moe_shape* s) {
+  const size_t rows = (size_t)(s->T * s->K);
+  const size_t b = align_up(rows * 2 * s->F, 256) + align_up(rows * fp8_scale_ld(2 * s->F), 256);
+  return b < 256 ? 256 : b;
+}
+
+int launch_ffn_fwd_fp8(const moe_shape* s, const void* xq, const uint8_t* xs,
+                       const int32_t* xrows, const int32_t* offsets,
+                       const int32_t* tile_offsets, const moe_fp8_weights* w, void* h, void* a,
+                       void* yp, void* ws, hipStream_t st) {
+  return s->dtype == MOE_BF16
+             ? ffn_fwd_t<BF16>(s, xq, xs, xrows, offsets, tile_offsets, w, h, a, yp, ws, st)
+             : ffn_fwd_t<F16>(s, xq, xs, xrows, offsets, tile_offsets, w, h, a, yp, ws, st);
+}
+
+int launch_ffn_dgrad_fp8(const moe_shape* s, const void* dq, const uint8_t* ds,
+                         const int32_t* xrows, const float* gates, const void* h,
+                         const int32_t* offsets, const int32_t* tile_offsets,
+                         const moe_fp8_weights* w, void* dh, void* dxp, void* ag, void* ws,
+                         hipStream_t st) {
+  return s->dtype == MOE_BF16 ? ffn_dgrad_t<BF16>(s, dq, ds, xrows, gates, h, offsets,
+                                                  tile_offsets, w, dh, dxp, ag, ws, st)
+                              : ffn_dgrad_t<F16>(s, dq, ds, xrows, gates, h, offsets,
+                                                 tile_offsets, w, dh, dxp, ag, ws, st);
+}
+
+}  // namespace moe

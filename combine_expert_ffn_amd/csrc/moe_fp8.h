@@ -1,0 +1,71 @@
+// Internal declarations of the 8-bit expert path and the weight update.
+#pragma once
+
+#include "moe_internal.h"
+
+namespace moe {
+
+int validate_shape(const moe_shape* s);  // abi.cpp
+
+// Bytes per row of scales for k values: a multiple of 4, so that four blocks'
+// scales are one aligned 32-bit load.
+inline int64_t fp8_scale_ld(int64_t k) { return (cdiv(k, MOE_FP8_BLOCK) + 3) / 4 * 4; }
+
+// ---------------------------------------------------------------------------
+// the block format
+// ---------------------------------------------------------------------------
+// Scale byte of a block with largest finite magnitude amax (>= 0): the biased
+// exponent of the smallest power of two with amax <= 448 * 2^(byte - 127).
+// 448 = 1.75 * 2^8, so the exponent is amax's own less 8, one more if its
+// mantissa is above 1.75 (adding 0x1fffff carries exactly then).
+__device__ __forceinline__ int fp8_scale_byte(float amax) {
+  const int b = (int)((__float_as_uint(amax) + 0x1fffffu) >> 23) - 8;
+  return amax == 0.f ? 127 : (b < 0 ? 0 : b);
+}
+// 2^(127 - byte), the factor into the block's units; byte <= 247 for a finite
+// amax, so it is a normal float.
+__device__ __forceinline__ float fp8_inv_scale(int byte) {
+  return __uint_as_float((uint32_t)(254 - byte) << 23);
+}
+// 2^(byte - 127); subnormal for byte 0.
+__device__ __forceinline__ float fp8_scale_value(int byte) {
+  return byte == 0 ? __uint_as_float(0x00400000u) : __uint_as_float((uint32_t)byte << 23);
+}
+// |x| for finite x, else 0.
+__device__ __forceinline__ float finite_abs(float x) {
+  const float a = fabsf(x);
+  return a < __builtin_inff() ? a : 0.f;
+}
+// Four floats in the block's units -> four e4m3 bytes, to nearest even
+// (v_cvt_pk_fp8_f32; magnitudes are at most 448, and an infinity is made a NaN
+// by the caller's finite_or_nan).
+__device__ __forceinline__ uint32_t pack_fp8(float a, float b, float c, float d) {
+  int v = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false);
+  v = __builtin_amdgcn_cvt_pk_fp8_f32(c, d, v, true);
+  return (uint32_t)v;
+}
+__device__ __forceinline__ float finite_or_nan(float x) {
+  return fabsf(x) < __builtin_inff() ? x : __builtin_nanf("");
+}
+
+// ---------------------------------------------------------------------------
+// launchers
+// ---------------------------------------------------------------------------
+int launch_quant_rows(const moe_shape* s, const void* src, int64_t rows, const int32_t* n_rows,
+                      void* q, uint8_t* qs, hipStream_t st);
+int launch_quant_weights(const moe_shape* s, const void* W_gu, const void* W_down,
+                         const moe_fp8_weights* w, hipStream_t st);
+// The 8-bit experts.  ws: q of a (or dh) [T*K][F] ([T*K][2F]), then its scales.
+size_t fp8_workspace_bytes(const moe_shape* s);
+int launch_ffn_fwd_fp8(const moe_shape* s, const void* xq, const uint8_t* xs,
+                       const int32_t* xrows, const int32_t* offsets,
+                       const int32_t* tile_offsets, const moe_fp8_weights* w, void* h, void* a,
+                       void* yp, void* ws, hipStream_t st);
+int launch_ffn_dgrad_fp8(const moe_shape* s, const void* dq, const uint8_t* ds,
+                         const int32_t* xrows, const float* gates, const void* h,
+                         const int32_t* offsets, const int32_t* tile_offsets,
+                         const moe_fp8_weights* w, void* dh, void* dxp, void* ag, void* ws,
+                         hipStream_t st);
+int launch_adamw(const moe_adamw_tensor* t, int n, const moe_adamw_hyper* hp, hipStream_t st);
+
+}  // namespace moe

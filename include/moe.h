@@ -506,6 +506,158 @@ int moe_shared_expert_wgrad(const moe_shape* s, int64_t F_s, const void* x, cons
                             float* dW_down_s, int accumulate, void* ws, size_t ws_bytes,
                             hipStream_t stream);
 
+/* ---- experts on 8-bit operands --------------------------------------------- */
+/*
+ * The routed experts' products on 8-bit operands.  A quantised matrix holds
+ * e4m3 values q (the OCP 8-bit float with four exponent and three mantissa
+ * bits, largest value 448, no infinities) and one scale byte s per block of
+ * MOE_FP8_BLOCK values along the product's reduction axis; it stands for
+ *   q * 2^(s - 127).
+ * A scale is the smallest power of two with max|x| <= 448 * scale over the
+ * block's finite values (s = 127 for a block of zeros, never below 0), and
+ * q = x / scale rounded to nearest even; a value that is not finite becomes
+ * the e4m3 NaN.  Powers of two divide exactly and are what the matrix
+ * instructions of gfx950 apply themselves, so a block's scale costs no
+ * arithmetic.  Activations have a scale per row and 128 columns, weights one
+ * per 128 x 128 (so a transposed copy holds the same values).
+ *   Scale rows are padded to moe_fp8_scale_ld(k) bytes for k values (k / 128
+ * rounded up to a multiple of 4; the padding is written as 0).
+ *   All calls here need d and F to be multiples of 128 (MOE_ERR_SHAPE); the
+ * products need 16-bit data, MOE_BF16 or MOE_F16 (MOE_ERR_UNSUPPORTED).
+ *   q buffers and workspaces are 16-byte aligned, scale buffers 4-byte
+ * (MOE_ERR_ARG).
+ */
+#define MOE_FP8_BLOCK 128
+
+/* Bytes per row of scales of a matrix with k values per row. */
+int64_t moe_fp8_scale_ld(int64_t k);
+
+/* The routed experts' weights in 8 bits, as moe_quant_weights_fp8 writes them
+ * (device pointers).  The transposed copies are read by moe_ffn_dgrad_fp8
+ * only; where just the forward runs their four pointers may be NULL. */
+typedef struct moe_fp8_weights {
+  void* gu;          /* [E_l,2F,d]             W_gu                         */
+  uint8_t* gu_s;     /* [E_l,2F/128,ld(d)]     ld = moe_fp8_scale_ld        */
+  void* down;        /* [E_l,d,F]              W_down                       */
+  uint8_t* down_s;   /* [E_l,d/128,ld(F)]                                   */
+  void* guT;         /* [E_l,d,2F]             W_gu transposed, or NULL     */
+  uint8_t* guT_s;    /* [E_l,d/128,ld(2F)]                                  */
+  void* downT;       /* [E_l,F,d]              W_down transposed, or NULL   */
+  uint8_t* downT_s;  /* [E_l,F/128,ld(d)]                                   */
+} moe_fp8_weights;
+
+/*
+ * moe_quant_rows_fp8 - quantise rows of hidden size d (token activations x or
+ * output gradients dout, or dispatched rows):
+ *   src [rows,d] dtype (any of the three), q [rows,d] e4m3, qs [rows,ld(d)].
+ *   n_rows: device pointer to the number of rows that exist (offsets + E_l for
+ *   dispatched rows), or NULL for all; later rows are left untouched.
+ *   0 <= rows < 2^31.  src is 16-byte aligned.
+ */
+int moe_quant_rows_fp8(const moe_shape* s, const void* src, int64_t rows, const int32_t* n_rows,
+                       void* q, uint8_t* qs, hipStream_t stream);
+
+/*
+ * moe_quant_weights_fp8 - quantise the experts' weights W_gu [E_l,2F,d] and
+ * W_down [E_l,d,F] (dtype, 16-byte aligned) in blocks of 128 x 128 into w,
+ * with the transposed copies if w has them (all four pointers or none,
+ * MOE_ERR_NULL).  Called after every weight update.
+ */
+int moe_quant_weights_fp8(const moe_shape* s, const void* W_gu, const void* W_down,
+                          const moe_fp8_weights* w, hipStream_t stream);
+
+/* Bytes of workspace moe_expert_ffn_fwd_fp8 and moe_ffn_dgrad_fp8 need. */
+size_t moe_fp8_workspace_bytes(const moe_shape* s);
+
+/*
+ * moe_expert_ffn_fwd_fp8 - moe_expert_ffn_fwd on quantised operands (X^ stands
+ * for quantised X).  Per local expert j:
+ *   [g,u] = x^ . W_gu^[j]^T,  a = silu(g) * u,  y_p = a^ . W_down^[j]^T
+ * with a^ quantised from the unrounded a, sums in float32.
+ *   xq, xs: with pair_of_row NULL the dispatched rows [T*K,d]; else the tokens
+ *   [T,d], and dispatched row r reads token pair_of_row[r] / K (as
+ *   moe_expert_ffn_fwd_gather; T*d must stay below 2^31).
+ *   h [T*K,2F], a [T*K,F] out (dtype), each may be NULL: h is what the dgrad
+ *   needs, a what moe_ffn_wgrad needs.  yp [T*K,d] out (dtype).
+ *   Rows >= N are untouched.  ws: moe_fp8_workspace_bytes.
+ */
+int moe_expert_ffn_fwd_fp8(const moe_shape* s, const void* xq, const uint8_t* xs,
+                           const int32_t* pair_of_row, const int32_t* offsets,
+                           const int32_t* tile_offsets, const moe_fp8_weights* w, void* h,
+                           void* a, void* yp, void* ws, size_t ws_bytes, hipStream_t stream);
+
+/*
+ * moe_ffn_dgrad_fp8 - moe_ffn_dgrad on quantised operands:
+ *   da = dyp^ . W_down^[j];  dh as moe_ffn_dgrad from da and the stored h;
+ *   dxp = dh^ . W_gu^[j]   with dh^ quantised from the unrounded dh
+ *   dq, ds: with pair_of_row NULL the quantised dyp by dispatched row [T*K,d]
+ *   (gates and ag are then NULL); else the quantised dout by token [T,d], and
+ *   as in moe_ffn_dgrad_gather da = gates[p] * (dout^[p / K] . W_down^[j]),
+ *   p = pair_of_row[r], gates [T*K] f32; ag [T*K,F] out may be NULL.
+ *   dh [T*K,2F] and dxp [T*K,d] out (dtype).  The weight gradient takes dh and
+ *   the 16-bit operands (moe_ffn_wgrad, moe_ffn_wgrad_fused): it is summed
+ *   over many micro-batches in float32 and stays out of 8 bits.
+ *   w needs the transposed copies.  ws: moe_fp8_workspace_bytes.
+ */
+int moe_ffn_dgrad_fp8(const moe_shape* s, const void* dq, const uint8_t* ds,
+                      const int32_t* pair_of_row, const float* gates, const void* h,
+                      const int32_t* offsets, const int32_t* tile_offsets,
+                      const moe_fp8_weights* w, void* dh, void* dxp, void* ag, void* ws,
+                      size_t ws_bytes, hipStream_t stream);
+
+/* ---- weight update --------------------------------------------------------- */
+/*
+ * One tensor of an AdamW step (device pointers).  The state is float32, or, with
+ * state8, e4m3 values in blocks of 128 consecutive elements with a scale byte
+ * each (as above): m holds the first moment, v the square root of the second.
+ */
+typedef struct moe_adamw_tensor {
+  int64_t n;          /* elements, 0 <= n < 2^36                               */
+  void* param;        /* [n] dtype: the weights, overwritten                   */
+  float* master;      /* [n] float32 weights the step updates (param gets them
+                         rounded), or NULL: param itself is read and updated   */
+  const float* grad;  /* [n] gradient                                          */
+  void* m;            /* [n] float32, or e4m3 with state8                      */
+  void* v;            /* [n] float32, or e4m3 of sqrt(v) with state8           */
+  uint8_t* m_s;       /* [ceil(n/128)] with state8, else NULL                  */
+  uint8_t* v_s;       /* [ceil(n/128)] with state8, else NULL                  */
+  int32_t dtype;      /* of param: MOE_F32, MOE_BF16 or MOE_F16                */
+  int32_t state8;     /* 0 or 1                                                */
+  float weight_decay;
+  int32_t reserved;   /* 0                                                     */
+} moe_adamw_tensor;
+
+typedef struct moe_adamw_hyper {
+  double lr, beta1, beta2, eps;  /* 0 <= beta < 1, eps > 0, lr finite          */
+  int64_t step;                  /* number of this step, from 1                */
+  uint64_t seed;                 /* of the random rounding (state8)            */
+  const float* grad_scale_dev;   /* device scalar that multiplies the gradients
+                                    (a clipping factor), or NULL               */
+  float grad_scale;              /* host factor of the gradients               */
+  int32_t reserved;              /* 0                                          */
+} moe_adamw_hyper;
+
+/*
+ * moe_adamw - one AdamW step over n tensors (t: host array, any mix of types
+ * and sizes):
+ *   g = grad_scale * [*grad_scale_dev] * grad
+ *   m = beta1 m + (1 - beta1) g;  v = beta2 v + (1 - beta2) g^2
+ *   p = (1 - lr wd) p - lr / (1 - beta1^step) * m
+ *                       / (sqrt(v) / sqrt(1 - beta2^step) + eps)
+ * in float32 from the unrounded m and v.  8-bit states are rounded up or down at
+ * random with the right mean (to nearest, an average that moves by 1 - beta2
+ * of itself would never leave a value with four significant bits): a 20-bit
+ * number made from (seed, step, index of the tensor in t, element) is added
+ * below the last kept bit, so equal arguments give equal results.
+ *   Tensors must not overlap, and each pointer is aligned to its element type.
+ * The hyperparameters are read by the host: a captured graph replays the step
+ * number and the learning rate it was captured with.  Empty tensors
+ * (and an empty list) are skipped.  Errors: MOE_ERR_NULL, MOE_ERR_SHAPE
+ * (n < 0 or a tensor of 2^36 elements or more), MOE_ERR_DTYPE, MOE_ERR_ARG
+ * (hyperparameters, alignment, reserved fields, scales given without state8).
+ */
+int moe_adamw(const moe_adamw_tensor* t, int n, const moe_adamw_hyper* hp, hipStream_t stream);
+
 /* ---- two-micro-batch step ------------------------------------------------ */
 /* One micro-batch's buffers (sizes as in the calls above). */
 typedef struct moe_mb {
