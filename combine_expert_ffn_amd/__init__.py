@@ -443,6 +443,32 @@ def moe_dispatch_bwd(s, dxp, row_of_pair, idx, dlogits, W_r, dx, accumulate, ws,
 
 
 # ---- experts on 8-bit operands ----------------------------------------------
+_DTYPES = {}
+
+
+def _chk_all(s, fn, tensors):
+    """_chk of several (name, tensor, kind, elements, optional), in one pass that
+    short calls can afford, and each on the current device."""
+    import torch
+
+    if not _DTYPES:
+        for dt in (MOE_F32, MOE_BF16, MOE_F16):
+            for kind in (_DATA, _F32, _I32, _FP8, _U8):
+                _DTYPES[kind, dt] = _torch_dtype(kind, MoeShape(dtype=dt))
+    dev, dt = None, s.dtype
+    for name, t, kind, numel, optional in tensors:
+        if t is None and optional:
+            continue
+        if not (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype is _DTYPES.get((kind, dt))
+                and t.is_contiguous() and t.numel() >= numel):
+            _chk(s, fn, name, t, kind, numel, optional)
+        if dev is None:
+            dev = torch.cuda.current_device()
+        if t.get_device() != dev:
+            raise MoeError(MOE_ERR_ARG, f"{fn}: {name} is on {t.device}, the current device is "
+                                        f"cuda:{dev}")
+
+
 def moe_fp8_scale_ld(k: int) -> int:
     """Bytes per row of scales of a matrix with k values per row."""
     return lib().moe_fp8_scale_ld(int(k))
@@ -455,19 +481,20 @@ def moe_fp8_workspace_bytes(s: MoeShape) -> int:
 class Fp8Weights:
     """The routed experts' weights in 8 bits for shape ``s`` (moe_fp8_weights in
     include/moe.h): e4m3 tensors gu, down (and transposed guT, downT) with their
-    uint8 scales.  Tensors not given are allocated; with ``transposed=False`` the
-    transposed copies, which only the dgrad reads, are left out."""
+    uint8 scales, allocated here, or given (gu, gu_s, down and down_s, and all four
+    transposed ones or none).  With ``transposed=False`` the transposed copies,
+    which only the dgrad reads, are not allocated."""
 
     def __init__(self, s: MoeShape, device="cuda", transposed=True, **tensors):
         import torch
 
         d, F, E_l = s.d, s.F, s.E_l
-        given_t = any(n.startswith(("guT", "downT")) for n in tensors)
-        if tensors and not given_t:
-            transposed = False
-        for n in tensors:
-            if n not in FP8_WEIGHT_FIELDS:
-                raise ValueError(f"Fp8Weights: unknown tensor {n}")
+        if tensors:
+            given = set(tensors)
+            transposed = given == set(FP8_WEIGHT_FIELDS)
+            if not transposed and given != {"gu", "gu_s", "down", "down_s"}:
+                raise ValueError(f"Fp8Weights: given {sorted(given)}, not gu, gu_s, down, down_s "
+                                 "(and the four transposed tensors)")
         b = MOE_FP8_BLOCK
         for n, rows, k in (("gu", 2 * F, d), ("down", d, F), ("guT", d, 2 * F), ("downT", F, d)):
             ld = (k // b + 3) // 4 * 4
@@ -478,14 +505,23 @@ class Fp8Weights:
                     t = torch.empty(shape, dtype=_torch_dtype(kind, s), device=device)
                 _chk(s, "Fp8Weights", name, t, kind, shape[0] * shape[1] * shape[2],
                      optional=n.endswith("T"))
+                if t is not None and name != "gu" and t.device != self.gu.device:
+                    raise MoeError(MOE_ERR_ARG, f"Fp8Weights: {name} is on {t.device}, gu on "
+                                                f"{self.gu.device}")
                 setattr(self, name, t)
         self.shape = (d, F, E_l)
+        self.device = self.gu.get_device()
         self.struct = MoeFp8Weights(*[_p(getattr(self, n)) for n in FP8_WEIGHT_FIELDS])
 
     def check(self, fn, s: MoeShape):
         if self.shape != (s.d, s.F, s.E_l):
             raise MoeError(MOE_ERR_ARG, f"{fn}: weights are for (d, F, E_l) = {self.shape}, the "
                                         f"shape has {(s.d, s.F, s.E_l)}")
+        import torch
+
+        if self.device != torch.cuda.current_device():
+            raise MoeError(MOE_ERR_ARG, f"{fn}: the weights are on cuda:{self.device}, not the "
+                                        "current device")
         return C.byref(self.struct)
 
 
@@ -493,29 +529,29 @@ def moe_quant_rows_fp8(s, src, rows, n_rows, q, qs, stream=None):
     """n_rows: None, or a device int32 tensor whose first element is the number
     of rows that exist."""
     fn, d = "moe_quant_rows_fp8", s.d
-    _chk(s, fn, "src", src, _DATA, rows * d)
-    _chk(s, fn, "n_rows", n_rows, _I32, 1, optional=True)
-    _chk(s, fn, "q", q, _FP8, rows * d)
-    _chk(s, fn, "qs", qs, _U8, rows * ((d // MOE_FP8_BLOCK + 3) // 4 * 4))
+    _chk_all(s, fn, (("src", src, _DATA, rows * d, False), ("n_rows", n_rows, _I32, 1, True),
+                     ("q", q, _FP8, rows * d, False),
+                     ("qs", qs, _U8, rows * ((d // MOE_FP8_BLOCK + 3) // 4 * 4), False)))
     check(lib().moe_quant_rows_fp8(C.byref(s), _p(src), int(rows), _p(n_rows), _p(q), _p(qs),
                                    _stream(stream)))
 
 
 def moe_quant_weights_fp8(s, W_gu, W_down, w: Fp8Weights, stream=None):
     fn, d, F, E_l = "moe_quant_weights_fp8", s.d, s.F, s.E_l
-    _chk(s, fn, "W_gu", W_gu, _DATA, E_l * 2 * F * d)
-    _chk(s, fn, "W_down", W_down, _DATA, E_l * d * F)
+    _chk_all(s, fn, (("W_gu", W_gu, _DATA, E_l * 2 * F * d, False),
+                     ("W_down", W_down, _DATA, E_l * d * F, False)))
     check(lib().moe_quant_weights_fp8(C.byref(s), _p(W_gu), _p(W_down), w.check(fn, s),
                                       _stream(stream)))
 
 
-def _chk_fp8(s, fn, q, qs, pair_of_row, offsets, tile_offsets, ws):
-    rows = s.T * s.K if pair_of_row is None else s.T
-    _chk(s, fn, "quantised rows", q, _FP8, rows * s.d)
-    _chk(s, fn, "row scales", qs, _U8, rows * ((s.d // MOE_FP8_BLOCK + 3) // 4 * 4))
-    _chk(s, fn, "pair_of_row", pair_of_row, _I32, s.T * s.K, optional=True)
-    _chk(s, fn, "offsets", offsets, _I32, s.E_l + 1)
-    _chk(s, fn, "tile_offsets", tile_offsets, _I32, s.E_l + 1)
+def _chk_fp8(s, fn, q, qs, pair_of_row, offsets, tile_offsets, ws, more):
+    cap, d = s.T * s.K, s.d
+    rows = cap if pair_of_row is None else s.T
+    _chk_all(s, fn, (("quantised rows", q, _FP8, rows * d, False),
+                     ("row scales", qs, _U8, rows * ((d // MOE_FP8_BLOCK + 3) // 4 * 4), False),
+                     ("pair_of_row", pair_of_row, _I32, cap, True),
+                     ("offsets", offsets, _I32, s.E_l + 1, False),
+                     ("tile_offsets", tile_offsets, _I32, s.E_l + 1, False)) + more)
     _chk_ws(fn, ws)
 
 
@@ -524,10 +560,9 @@ def moe_expert_ffn_fwd_fp8(s, xq, xs, pair_of_row, offsets, tile_offsets, w: Fp8
     """pair_of_row None: xq, xs hold the dispatched rows; else the tokens.  h and
     a may be None (not written)."""
     fn, cap, d, F = "moe_expert_ffn_fwd_fp8", s.T * s.K, s.d, s.F
-    _chk_fp8(s, fn, xq, xs, pair_of_row, offsets, tile_offsets, ws)
-    _chk(s, fn, "h", h, _DATA, cap * 2 * F, optional=True)
-    _chk(s, fn, "a", a, _DATA, cap * F, optional=True)
-    _chk(s, fn, "yp", yp, _DATA, cap * d)
+    _chk_fp8(s, fn, xq, xs, pair_of_row, offsets, tile_offsets, ws,
+             (("h", h, _DATA, cap * 2 * F, True), ("a", a, _DATA, cap * F, True),
+              ("yp", yp, _DATA, cap * d, False)))
     wp, wb = _ws(ws)
     check(lib().moe_expert_ffn_fwd_fp8(C.byref(s), _p(xq), _p(xs), _p(pair_of_row), _p(offsets),
                                        _p(tile_offsets), w.check(fn, s), _p(h), _p(a), _p(yp),
@@ -539,12 +574,10 @@ def moe_ffn_dgrad_fp8(s, dq, ds, pair_of_row, gates, h, offsets, tile_offsets, w
     """pair_of_row None: dq, ds hold the quantised dyp by dispatched row (gates and
     ag None); else the quantised dout by token, with the pairs' gates."""
     fn, cap, d, F = "moe_ffn_dgrad_fp8", s.T * s.K, s.d, s.F
-    _chk_fp8(s, fn, dq, ds, pair_of_row, offsets, tile_offsets, ws)
-    _chk(s, fn, "gates", gates, _F32, cap, optional=True)
-    _chk(s, fn, "h", h, _DATA, cap * 2 * F)
-    _chk(s, fn, "dh", dh, _DATA, cap * 2 * F)
-    _chk(s, fn, "dxp", dxp, _DATA, cap * d)
-    _chk(s, fn, "ag", ag, _DATA, cap * F, optional=True)
+    _chk_fp8(s, fn, dq, ds, pair_of_row, offsets, tile_offsets, ws,
+             (("gates", gates, _F32, cap, True), ("h", h, _DATA, cap * 2 * F, False),
+              ("dh", dh, _DATA, cap * 2 * F, False), ("dxp", dxp, _DATA, cap * d, False),
+              ("ag", ag, _DATA, cap * F, True)))
     wp, wb = _ws(ws)
     check(lib().moe_ffn_dgrad_fp8(C.byref(s), _p(dq), _p(ds), _p(pair_of_row), _p(gates), _p(h),
                                   _p(offsets), _p(tile_offsets), w.check(fn, s), _p(dh), _p(dxp),
@@ -564,6 +597,7 @@ class AdamWTensors:
         fn = "AdamWTensors"
         dts = {torch.float32: MOE_F32, torch.bfloat16: MOE_BF16, torch.float16: MOE_F16}
         self.tensors = [dict(t) for t in tensors]
+        self.device = None
         self.array = (MoeAdamwTensor * max(1, len(self.tensors)))()
         for i, t in enumerate(self.tensors):
             p = t["param"]
@@ -571,6 +605,8 @@ class AdamWTensors:
                 raise MoeError(MOE_ERR_DTYPE, f"{fn}: param {i} must be a float32, bfloat16 or "
                                               "float16 tensor")
             n, q8 = p.numel(), t["m"].dtype == torch.float8_e4m3fn
+            if self.device is None:
+                self.device = p.device
             s = MoeShape(dtype=dts[p.dtype])
             nb = -(-n // MOE_FP8_BLOCK)
             for name, kind, want, opt in (
@@ -580,9 +616,9 @@ class AdamWTensors:
                     ("v_s", _U8, nb, not q8)):
                 x = t.get(name)
                 _chk(s, fn, f"{name} {i}", x, kind, want, optional=opt)
-                if x is not None and (x.numel() != want or x.device != p.device):
+                if x is not None and (x.numel() != want or x.device != self.device):
                     raise MoeError(MOE_ERR_ARG, f"{fn}: {name} {i} has {x.numel()} elements on "
-                                                f"{x.device}, needs {want} on {p.device}")
+                                                f"{x.device}, needs {want} on {self.device}")
             self.array[i] = MoeAdamwTensor(
                 n, *[_p(t.get(k)) for k in ("param", "master", "grad", "m", "v", "m_s", "v_s")],
                 s.dtype, int(q8), float(t.get("weight_decay", 0.0)), 0)
@@ -593,8 +629,15 @@ def moe_adamw(tensors, lr, beta1=0.9, beta2=0.999, eps=1e-8, step=1, grad_scale=
     """tensors: an AdamWTensors (or the list of dicts to make one of)."""
     if not isinstance(tensors, AdamWTensors):
         tensors = AdamWTensors(tensors)
-    _chk(MoeShape(dtype=MOE_F32), "moe_adamw", "grad_scale_dev", grad_scale_dev, _F32, 1,
-         optional=True)
+    if grad_scale_dev is not None:
+        _chk_all(MoeShape(dtype=MOE_F32), "moe_adamw",
+                 (("grad_scale_dev", grad_scale_dev, _F32, 1, False),))
+    if tensors.device is not None:
+        import torch
+
+        if tensors.device.index != torch.cuda.current_device():
+            raise MoeError(MOE_ERR_ARG, f"moe_adamw: the tensors are on {tensors.device}, not the "
+                                        "current device")
     hp = MoeAdamwHyper(lr, beta1, beta2, eps, int(step), int(seed) & (2 ** 64 - 1),
                        _p(grad_scale_dev), grad_scale, 0)
     check(lib().moe_adamw(tensors.array, len(tensors.tensors), C.byref(hp), _stream(stream)))

@@ -19,7 +19,8 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD_DIR = os.path.join(ROOT, "_build")
 LIB = os.path.join(HERE, "libmoe.so")
 SOURCES = ["abi.cpp", "route.hip", "dispatch.hip", "gemm_mfma.hip", "gemm_simt.hip",
-           "abi_fp8.cpp", "quant_fp8.hip", "gemm_fp8.hip", "adamw.hip"]
+           "abi_fp8.cpp", "quant_fp8.hip", "gemm_fp8.hip", "gemm_fp8_small.hip",
+           "adamw.hip"]
 
 
 def hipcc() -> str:

@@ -554,6 +554,7 @@ int ffn_dgrad_t(const moe_shape* s, const void* dq, const uint8_t* ds, const int
 }  // namespace
 
 size_t fp8_workspace_bytes(const moe_shape* s) {
+  if (fp8_small(s)) return align_up(fp8_small_workspace_bytes(s) + 256, 256);
   const size_t rows = (size_t)(s->T * s->K);
   const size_t b = align_up(rows * 2 * s->F, 256) + align_up(rows * fp8_scale_ld(2 * s->F), 256);
   return b < 256 ? 256 : b;
@@ -563,6 +564,8 @@ int launch_ffn_fwd_fp8(const moe_shape* s, const void* xq, const uint8_t* xs,
                        const int32_t* xrows, const int32_t* offsets,
                        const int32_t* tile_offsets, const moe_fp8_weights* w, void* h, void* a,
                        void* yp, void* ws, hipStream_t st) {
+  if (fp8_small(s))
+    return launch_ffn_fwd_fp8_small(s, xq, xs, xrows, offsets, w, h, a, yp, ws, st);
   return s->dtype == MOE_BF16
              ? ffn_fwd_t<BF16>(s, xq, xs, xrows, offsets, tile_offsets, w, h, a, yp, ws, st)
              : ffn_fwd_t<F16>(s, xq, xs, xrows, offsets, tile_offsets, w, h, a, yp, ws, st);
@@ -573,6 +576,8 @@ int launch_ffn_dgrad_fp8(const moe_shape* s, const void* dq, const uint8_t* ds,
                          const int32_t* offsets, const int32_t* tile_offsets,
                          const moe_fp8_weights* w, void* dh, void* dxp, void* ag, void* ws,
                          hipStream_t st) {
+  if (fp8_small(s))
+    return launch_ffn_dgrad_fp8_small(s, dq, ds, xrows, gates, h, offsets, w, dh, dxp, ag, ws, st);
   return s->dtype == MOE_BF16 ? ffn_dgrad_t<BF16>(s, dq, ds, xrows, gates, h, offsets,
                                                   tile_offsets, w, dh, dxp, ag, ws, st)
                               : ffn_dgrad_t<F16>(s, dq, ds, xrows, gates, h, offsets,

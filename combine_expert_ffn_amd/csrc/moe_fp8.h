@@ -66,6 +66,17 @@ int launch_ffn_dgrad_fp8(const moe_shape* s, const void* dq, const uint8_t* ds,
                          const int32_t* offsets, const int32_t* tile_offsets,
                          const moe_fp8_weights* w, void* dh, void* dxp, void* ag, void* ws,
                          hipStream_t st);
+// The same for few rows per expert (gemm_fp8_small.hip), and the rule that takes it.
+bool fp8_small(const moe_shape* s);
+size_t fp8_small_workspace_bytes(const moe_shape* s);
+int launch_ffn_fwd_fp8_small(const moe_shape* s, const void* xq, const uint8_t* xs,
+                             const int32_t* xrows, const int32_t* offsets,
+                             const moe_fp8_weights* w, void* h, void* a, void* yp, void* ws,
+                             hipStream_t st);
+int launch_ffn_dgrad_fp8_small(const moe_shape* s, const void* dq, const uint8_t* ds,
+                               const int32_t* xrows, const float* gates, const void* h,
+                               const int32_t* offsets, const moe_fp8_weights* w, void* dh,
+                               void* dxp, void* ag, void* ws, hipStream_t st);
 int launch_adamw(const moe_adamw_tensor* t, int n, const moe_adamw_hyper* hp, hipStream_t st);
 
 }  // namespace moe
