@@ -1,14 +1,15 @@
 // Grouped expert products on 8-bit operands (gfx950): e4m3 values with a
-// power-of-two scale per 128 along the reduction, float32 accumulation
-// (v_mfma_scale_f32_32x32x64_f8f6f4).  The instruction multiplies each lane's
-// 32 values by a scale byte of that lane's own, so the block scales of both
-// operands enter without a vector instruction and every block's products go
-// into the one accumulator.
+// power-of-two scale per 128 along the reduction, float32 accumulation.
 //
-// A stage of the reduction is one block of 128 values = 128 bytes per row, the
-// bytes of 64 values in 16 bits, and a 32 x 32 x 64 instruction takes 64 cycles
-// for 64 bytes of each row as the 16-bit one takes 32 for 32: the tile that
-// balances LDS reads against the matrix cores there does so here.
+// bf16 data: v_mfma_scale_f32_32x32x64_f8f6f4 multiplies each lane's 32 values by
+// a scale byte of that lane's own, so the block scales of both operands enter
+// without a vector instruction.  It aligns a group of products to the group's
+// largest and drops what lies below (measured: 5e-5 of a sum, against bf16's 2e-3).
+// fp16 data, whose results keep 11 bits: the values are widened to bf16 with their
+// scale (exact, one instruction per two) and multiplied by
+// v_mfma_f32_32x32x16_bf16 at half the rate.
+//
+// A stage of the reduction is one block of 128 values = 128 bytes per row.
 //  * block tile 256 x 256, 8 waves (2 per SIMD) of 64 x 128 = 2 x 4 MFMA tiles;
 //    a wave's 128 columns are whole scale blocks of the output, so the fused
 //    quantisation needs at most one exchange with another wave;
@@ -16,7 +17,14 @@
 //    by the row; a lane's 32 bytes are the chunks 2t + lane / 32 of two
 //    consecutive pairs t, the same for both operands (the order of the values
 //    within a block does not change its sum);
+//  * stages are copied from memory straight to LDS, one ahead; 128-byte rows, since
+//    64-byte pieces halve the rate of L2 (17 against 34 TB/s);
+//  * outputs are staged through LDS to rows of 128 bytes or more and stored past
+//    L2 (non-temporal), where they would push out the operands that 32 CUs share;
 //  * persistent grid over the dispatch plan's row tiles, one range per XCD.
+// What bounds it: the LDS traffic of a stage (192 KB read, 64 KB written) takes the
+// LDS as long as its MFMAs take the matrix cores, and loads and stores of a CU
+// share one queue, so a tile's stores (write rate of HBM) add to its loads.
 #include "moe_fp8.h"
 
 namespace moe {
@@ -24,11 +32,20 @@ namespace {
 
 typedef int i32x4_t __attribute__((ext_vector_type(4)));
 typedef int i32x8_t __attribute__((ext_vector_type(8)));
+typedef unsigned int u32x2_t __attribute__((ext_vector_type(2)));
 typedef unsigned int u32x4_t __attribute__((ext_vector_type(4)));
 typedef float f32x16_t __attribute__((ext_vector_type(16)));
+typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
+typedef __attribute__((address_space(3))) uint8_t lds_u8_t;
 
-struct BF16 { typedef uint16_t elt; };
-struct F16 { typedef _Float16 elt; };
+struct BF16 {
+  typedef uint16_t elt;
+  static constexpr bool WIDE = false;
+};
+struct F16 {
+  typedef _Float16 elt;
+  static constexpr bool WIDE = true;
+};
 
 constexpr int BM = 256, BN = 256, NT = 512;
 constexpr int WGN = 2;                    // waves along N; 4 along M
@@ -36,10 +53,13 @@ constexpr int WTM = 64, WTN = 128;        // wave tile
 constexpr int TM = WTM / 32, TN = WTN / 32;
 constexpr int STAGE = BM * 128;           // bytes of one operand's stage
 static_assert(BM == kTileM, "row tiles come from the dispatch plan");
-// Epilogue staging: 32 rows x 128 columns of floats per wave, rows 132 apart.
+// Epilogue staging: 16 rows x 128 columns of floats per wave, rows 132 apart, in
+// the second stage's buffer and a little past it (the first takes the next tile's
+// first stage meanwhile).
 constexpr int EP_LD = 132;
-constexpr int SMEM = NT / 64 * 32 * EP_LD * 4;
-static_assert(SMEM >= 4 * STAGE, "the stages fit the epilogue's LDS");
+constexpr int EP_WAVE = 16 * EP_LD * 4;
+constexpr int SMEM = 2 * STAGE + NT / 64 * EP_WAVE;
+static_assert(SMEM >= 4 * STAGE, "two stages of both operands");
 
 __device__ __forceinline__ int swz(int row) { return (row & 7) ^ ((row >> 3) & 1); }
 
@@ -48,32 +68,45 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc_of(const void* p) {
   return __builtin_amdgcn_make_buffer_rsrc((void*)p, (short)0, 0x7fffffff, 0x00020000);
 }
 
-// One operand's 256 rows: 4 chunks of 16 bytes per thread and stage, chunk c
-// at tile row c * 64 + tid / 8, 16-byte chunk tid % 8.
+// One operand's 256 rows, copied straight to LDS (no registers in between): 4
+// instructions per wave and stage, each writing 1024 consecutive bytes = 8 tile
+// rows; lane l's 16 bytes land at chunk l % 8 of row l / 8, so the lane reads
+// the chunk that the swizzle puts there.  The copies are inline assembly: the
+// compiler would wait for all of them ahead of every LDS read; here stage_wait()
+// does, once per stage.
 struct Load {
-  u32x4_t v[4];
-  __amdgpu_buffer_rsrc_t rsrc;
+  u32x4_t rsrc;
   uint32_t off[4];
-  int dst0;
   template <class RowOff>
   __device__ __forceinline__ void init(const void* base, RowOff row_off, int tid) {
-    rsrc = rsrc_of(base);
-#pragma unroll
-    for (int c = 0; c < 4; ++c)
-      off[c] = (uint32_t)row_off(c * 64 + (tid >> 3)) + (uint32_t)(tid & 7) * 16u;
+    const uint64_t p = (uint64_t)base;
+    // raw buffer (stride 0); every offset used is a valid byte of the operand
+    rsrc = u32x4_t{(uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)p),
+                   (uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)(p >> 32)) & 0xffffu,
+                   0x7fffffffu, 0x00020000u};
     const int row = tid >> 3;  // rows 64 apart have the same swizzle
-    dst0 = row * 128 + (((tid & 7) ^ swz(row)) << 4);
-  }
-  __device__ __forceinline__ void load(int kt) {
 #pragma unroll
     for (int c = 0; c < 4; ++c)
-      v[c] = __builtin_amdgcn_raw_buffer_load_b128(rsrc, (int)off[c], kt * 128, 0);
+      off[c] = (uint32_t)row_off(c * 64 + row) + (uint32_t)((tid & 7) ^ swz(row)) * 16u;
   }
-  __device__ __forceinline__ void store(uint8_t* lds) const {
+  // stage kt to the LDS address of this wave's first 1024 bytes; on = false
+  // reads nothing (no byte of the buffer is in range; LDS gets zeros), without a
+  // branch, past which the compiler would sink the MFMAs before it
+  __device__ __forceinline__ void copy(int kt, uint32_t lds, bool on = true) const {
+    const u32x4_t r = {rsrc[0], rsrc[1], on ? rsrc[2] : 0u, rsrc[3]};
 #pragma unroll
-    for (int c = 0; c < 4; ++c) *(u32x4_t*)(lds + dst0 + c * 64 * 128) = v[c];
+    for (int c = 0; c < 4; ++c)
+      asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
+                   :
+                   : "s"(lds + c * 64 * 128), "v"(off[c]), "s"(r), "s"(kt * 128)
+                   : "memory");
   }
 };
+// Waits until at most N of the wave's memory operations are outstanding.
+template <int N>
+__device__ __forceinline__ void stage_wait() {
+  asm volatile("s_waitcnt vmcnt(%0)" : : "n"(N) : "memory");
+}
 
 // Scale bytes of four stages at a time: of the wave's rows (one per lane and
 // 32-row tile) and of the two 64-column halves of its columns.
@@ -116,10 +149,73 @@ struct Pos {
   }
 };
 
-// The reduction over nk stages, once stage 0 is in LDS buffer 0 and stage 1 in
-// the loaders' registers.  Ends with a barrier: the LDS is free.
-__device__ __forceinline__ void mainloop(Load& la, Load& lb, Scales& sc, int nk, uint8_t* smem,
-                                         f32x16_t (&acc)[TM][TN]) {
+// Eight e4m3 values (two registers) times a power of two, exact in bf16.
+__device__ __forceinline__ bf16x8_t widen(int lo, int hi, float scale) {
+  const bf16x2_t a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, scale, false);
+  const bf16x2_t b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, scale, true);
+  const bf16x2_t c = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, scale, false);
+  const bf16x2_t d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, scale, true);
+  return bf16x8_t{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
+}
+
+// One 64-deep slice: the MFMAs of the wave on a and b, and beside them the reads
+// of the next slice's fragments (an into its own registers, b's four one by one
+// into those the MFMAs are done with).
+template <bool WIDE>
+__device__ __forceinline__ void slice(const i32x8_t (&a)[TM], i32x8_t (&an)[TM], i32x8_t (&b)[TN],
+                                      const uint32_t (&sa)[TM], const uint32_t (&sb)[2],
+                                      f32x16_t (&acc)[TM][TN], const uint8_t* next, int kk,
+                                      const Pos& w) {
+  auto next_b = [&](int j) {
+    return read_frag(next + STAGE, w.wn * WTN + j * 32, kk, w.lane);
+  };
+  auto next_a = [&]() {
+#pragma unroll
+    for (int i = 0; i < TM; ++i) an[i] = read_frag(next, w.wm * WTM + i * 32, kk, w.lane);
+  };
+  if constexpr (WIDE) {
+    float fa[TM], fb[2];
+#pragma unroll
+    for (int i = 0; i < TM; ++i) fa[i] = fp8_scale_value((int)(sa[i] & 255u));
+#pragma unroll
+    for (int j = 0; j < 2; ++j) fb[j] = fp8_scale_value((int)(sb[j] & 255u));
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      bf16x8_t aw[TM];
+#pragma unroll
+      for (int i = 0; i < TM; ++i) aw[i] = widen(a[i][2 * q], a[i][2 * q + 1], fa[i]);
+      if (q == 2) next_a();
+#pragma unroll
+      for (int j = 0; j < TN; ++j) {
+        const bf16x8_t bw = widen(b[j][2 * q], b[j][2 * q + 1], fb[j >> 1]);
+#pragma unroll
+        for (int i = 0; i < TM; ++i)
+          acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(aw[i], bw, acc[i][j], 0, 0, 0);
+        if (q == 3) b[j] = next_b(j);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    }
+  } else {
+    i32x8_t bn[TN];
+#pragma unroll
+    for (int j = 0; j < TN; ++j) {
+      if (j == 0) next_a();
+      if (j > 0) bn[j - 1] = next_b(j - 1);
+      if (j == TN - 1) bn[j] = next_b(j);
+#pragma unroll
+      for (int i = 0; i < TM; ++i)
+        acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
+            a[i], b[j], acc[i][j], 0, 0, 0, (int)sa[i], 0, (int)sb[j >> 1]);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+#pragma unroll
+    for (int j = 0; j < TN; ++j) b[j] = bn[j];
+  }
+}
+
+template <bool WIDE>
+__device__ __forceinline__ void mainloop(const Load& la, const Load& lb, Scales& sc, int nk,
+                                         uint8_t* smem, uint32_t lds, f32x16_t (&acc)[TM][TN]) {
   const Pos w = Pos::of();
 #pragma unroll
   for (int i = 0; i < TM; ++i)
@@ -127,11 +223,17 @@ __device__ __forceinline__ void mainloop(Load& la, Load& lb, Scales& sc, int nk,
     for (int j = 0; j < TN; ++j)
 #pragma unroll
       for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.f;
+  i32x8_t a0[TM], a1[TM], b[TN];
+#pragma unroll
+  for (int i = 0; i < TM; ++i) a0[i] = read_frag(smem, w.wm * WTM + i * 32, 0, w.lane);
+#pragma unroll
+  for (int j = 0; j < TN; ++j) b[j] = read_frag(smem + STAGE, w.wn * WTN + j * 32, 0, w.lane);
   for (int kt = 0; kt < nk; ++kt) {
-    uint8_t* cur = smem + (kt & 1) * 2 * STAGE;
-    uint8_t* nxt = smem + (~kt & 1) * 2 * STAGE;
+    const int odd = kt & 1;
+    const uint8_t* cur = smem + odd * 2 * STAGE;
+    const uint8_t* nxt = smem + (odd ^ 1) * 2 * STAGE;
     if ((kt & 3) == 0) {
-      sc.next();
+      if (kt > 0) sc.next();
       sc.fetch(min(kt + 4, (nk - 1) & ~3));
     }
     const int sh = (kt & 3) * 8;
@@ -140,27 +242,17 @@ __device__ __forceinline__ void mainloop(Load& la, Load& lb, Scales& sc, int nk,
     for (int i = 0; i < TM; ++i) sa[i] = sc.a[i] >> sh;
     sb[0] = sc.b[0] >> sh;
     sb[1] = sc.b[1] >> sh;
-    la.store(nxt);
-    lb.store(nxt + STAGE);
-    const int k2 = min(kt + 2, nk - 1);
-    la.load(k2);
-    lb.load(k2);
-#pragma unroll
-    for (int kk = 0; kk < 2; ++kk) {
-      i32x8_t a[TM], b[TN];
-#pragma unroll
-      for (int i = 0; i < TM; ++i) a[i] = read_frag(cur, w.wm * WTM + i * 32, kk, w.lane);
-#pragma unroll
-      for (int j = 0; j < TN; ++j) b[j] = read_frag(cur + STAGE, w.wn * WTN + j * 32, kk, w.lane);
-#pragma unroll
-      for (int j = 0; j < TN; ++j)
-#pragma unroll
-        for (int i = 0; i < TM; ++i)
-          acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
-              a[i], b[j], acc[i][j], 0, 0, 0, (int)sa[i], 0, (int)sb[j >> 1]);
-    }
+    __builtin_amdgcn_sched_barrier(0);
+    slice<WIDE>(a0, a1, b, sa, sb, acc, cur, 1, w);
+    stage_wait<0>();
     __syncthreads();
+    la.copy(kt + 2, lds + odd * 2 * STAGE, kt + 2 < nk);
+    lb.copy(kt + 2, lds + odd * 2 * STAGE + STAGE, kt + 2 < nk);
+    __builtin_amdgcn_sched_barrier(0);
+    slice<WIDE>(a1, a0, b, sa, sb, acc, nxt, 0, w);
   }
+  stage_wait<0>();  // the copies past the last stage write zeros to LDS
+  __syncthreads();
 }
 
 // Persistent schedule: the blocks form G = min(8, grid) groups by block % G
@@ -178,18 +270,19 @@ struct Sched {
 };
 
 // (expert, first row, row end) of M-tile mt from LDS copies of the plan, in
-// scalar registers.
+// scalar registers: the expert is the number of later experts whose first tile is
+// not past mt, counted by all lanes at once.
 __device__ __forceinline__ void row_tile(const int* s_to, const int* s_off, int E_l, int mt,
                                          int& e, int& m0, int& m_end) {
-  int lo = 0, hi = E_l;  // s_to[lo] <= mt < s_to[hi]
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (s_to[mid] <= mt) lo = mid;
-    else hi = mid;
+  const int lane = (int)(threadIdx.x & 63);
+  e = 0;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const int j = 1 + k * 64 + lane;
+    e += (int)__popcll(__ballot(j < E_l && s_to[min(j, E_l)] <= mt));
   }
-  e = __builtin_amdgcn_readfirstlane(lo);
-  m0 = __builtin_amdgcn_readfirstlane(s_off[lo] + (mt - s_to[lo]) * kTileM);
-  m_end = __builtin_amdgcn_readfirstlane(s_off[lo + 1]);
+  m0 = __builtin_amdgcn_readfirstlane(s_off[e] + (mt - s_to[e]) * kTileM);
+  m_end = __builtin_amdgcn_readfirstlane(s_off[e + 1]);
 }
 
 // The row operand of a product: rows of the dispatched matrix, or token rows
@@ -233,17 +326,18 @@ struct Cols {
   }
 };
 
-// Accumulator tile i of this wave as 32 rows x 128 columns in the wave's own LDS
-// area (operations of one wave on LDS complete in order).
-__device__ __forceinline__ const float* stage_rows(const f32x16_t (&acc)[TM][TN], int i,
+// Rows 16 hb .. 16 hb + 15 of accumulator tile i of this wave (all four column tiles)
+// as rows of floats in the wave's own LDS area (operations of one wave on LDS complete in
+// order).
+__device__ __forceinline__ const float* stage_rows(const f32x16_t (&acc)[TM][TN], int i, int hb,
                                                    uint8_t* smem, const Pos& w) {
-  float* reg = reinterpret_cast<float*>(smem) + w.wave * 32 * EP_LD;
+  float* reg = reinterpret_cast<float*>(smem + 2 * STAGE + w.wave * EP_WAVE);
 #pragma unroll
   for (int j = 0; j < TN; ++j)
 #pragma unroll
-    for (int r = 0; r < 16; ++r)
+    for (int r = 0; r < 8; ++r)
       reg[(8 * (r >> 2) + 4 * (w.lane >> 5) + (r & 3)) * EP_LD + j * 32 + (w.lane & 31)] =
-          acc[i][j][r];
+          acc[i][j][hb * 8 + r];
   return reg;
 }
 __device__ __forceinline__ void ld8(const float* p, float* f) {
@@ -251,17 +345,37 @@ __device__ __forceinline__ void ld8(const float* p, float* f) {
   f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
   f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
 }
+// Stores past L2 (non-temporal).
+__device__ __forceinline__ void put16(void* p, const uint4& v) {
+  __builtin_nontemporal_store(__builtin_bit_cast(u32x4_t, v), (u32x4_t*)p);
+}
+__device__ __forceinline__ void put8(void* p, const uint2& v) {
+  __builtin_nontemporal_store(__builtin_bit_cast(u32x2_t, v), (u32x2_t*)p);
+}
+// Largest magnitude of eight values; NaN is passed over.
 __device__ __forceinline__ float amax8(const float* f) {
-  float m = 0.f;
+  float m = fmaxf(fabsf(f[0]), fabsf(f[1]));
 #pragma unroll
-  for (int t = 0; t < 8; ++t) m = fmaxf(m, finite_abs(f[t]));
+  for (int t = 2; t < 8; t += 2) m = fmaxf(fmaxf(fabsf(f[t]), fabsf(f[t + 1])), m);
+  return m;
+}
+// Where a lane's values hold an infinity (m, their largest magnitude, says so),
+// infinities are made NaN, which is what they are quantised to, and m the largest
+// of the rest.
+__device__ __forceinline__ float without_inf(float* f, float m) {
+  if (__any(m == __builtin_inff())) {
+    m = 0.f;
+#pragma unroll
+    for (int t = 0; t < 8; ++t) {
+      f[t] = finite_or_nan(f[t]);
+      m = fmaxf(m, finite_abs(f[t]));
+    }
+  }
   return m;
 }
 __device__ __forceinline__ uint2 quant8(const float* f, float inv) {
-  float y[8];
-#pragma unroll
-  for (int t = 0; t < 8; ++t) y[t] = finite_or_nan(f[t]) * inv;
-  return uint2{pack_fp8(y[0], y[1], y[2], y[3]), pack_fp8(y[4], y[5], y[6], y[7])};
+  return uint2{pack_fp8(f[0] * inv, f[1] * inv, f[2] * inv, f[3] * inv),
+               pack_fp8(f[4] * inv, f[5] * inv, f[6] * inv, f[7] * inv)};
 }
 // Largest value over rows of 8 or 16 lanes.
 template <int N>
@@ -281,6 +395,7 @@ __device__ __forceinline__ float lanes_max(float v) {
 // scale block per row; its two halves' largest magnitudes meet in LDS.
 template <class E>
 struct GateUpOp {
+  typedef E type;
   typedef typename E::elt elt;
   Rows x;
   Cols w;  // n = 2F
@@ -304,29 +419,30 @@ struct GateUpOp {
     const Pos p = Pos::of();
     const int c = (p.lane & 7) * 8, j0 = nt * 128 + p.wn * 64 + c;
     float av[TM][4][8];
+    const float* blk = nullptr;
 #pragma unroll
-    for (int i = 0; i < TM; ++i) {
-      const float* blk = stage_rows(acc, i, smem, p);
+    for (int i = 0; i < TM; ++i)
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
-        const int r = q * 8 + (p.lane >> 3), tr = p.wm * WTM + i * 32 + r;
+        if ((q & 1) == 0) blk = stage_rows(acc, i, q >> 1, smem, p);
+        const int r = (q & 1) * 8 + (p.lane >> 3), tr = p.wm * WTM + i * 32 + (q >> 1) * 16 + r;
         float g[8], u[8];
         ld8(blk + r * EP_LD + c, g);
         ld8(blk + r * EP_LD + 64 + c, u);
 #pragma unroll
         for (int t = 0; t < 8; ++t) av[i][q][t] = silu_fast(g[t]) * u[t];
-        const float mx = lanes_max<8>(amax8(av[i][q]));
-        if ((p.lane & 7) == 0) s_max[p.wn * BM + tr] = mx;
+        if (i == 0 && q == 0) stage_wait<0>();  // the next tile's stage, ahead of the stores
         if (m0 + tr < m_end) {
           const size_t row = (size_t)(m0 + tr);
           if (h) {
-            *(uint4*)(h + row * 2 * F + j0) = Chunk<elt>::pack(g);
-            *(uint4*)(h + row * 2 * F + F + j0) = Chunk<elt>::pack(u);
+            put16(h + row * 2 * F + j0, Chunk<elt>::pack(g));
+            put16(h + row * 2 * F + F + j0, Chunk<elt>::pack(u));
           }
-          if (a) *(uint4*)(a + row * F + j0) = Chunk<elt>::pack(av[i][q]);
+          if (a) put16(a + row * F + j0, Chunk<elt>::pack(av[i][q]));
         }
+        const float mx = lanes_max<8>(without_inf(av[i][q], amax8(av[i][q])));
+        if ((p.lane & 7) == 0) s_max[p.wn * BM + tr] = mx;
       }
-    }
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < TM; ++i)
@@ -336,7 +452,7 @@ struct GateUpOp {
         const int byte = fp8_scale_byte(fmaxf(s_max[tr], s_max[BM + tr]));
         if (m0 + tr < m_end) {
           const size_t row = (size_t)(m0 + tr);
-          *(uint2*)(aq + row * F + j0) = quant8(av[i][q], fp8_inv_scale(byte));
+          put8(aq + row * F + j0, quant8(av[i][q], fp8_inv_scale(byte)));
           if (p.wn == 0 && (p.lane & 7) == 0) as[row * ldF + nt] = (uint8_t)byte;
         }
       }
@@ -347,6 +463,7 @@ struct GateUpOp {
 // the second of the dgrad (dx_p = dh^ . W_gu, with the transposed weights).
 template <class E>
 struct PlainOp {
+  typedef E type;
   typedef typename E::elt elt;
   Rows x;
   Cols w;
@@ -361,18 +478,24 @@ struct PlainOp {
                                            int nt, uint8_t* smem, float*) const {
     const Pos p = Pos::of();
     const int cb = nt * BN + p.wn * WTN, c = (p.lane & 15) * 8;
-    if (cb >= w.n) return;  // wave-uniform; n is a multiple of 128
-#pragma unroll
-    for (int i = 0; i < TM; ++i) {
-      const float* blk = stage_rows(acc, i, smem, p);
-#pragma unroll
-      for (int q = 0; q < 8; ++q) {
-        const int r = q * 4 + (p.lane >> 4), row = m0 + p.wm * WTM + i * 32 + r;
-        float f[8];
-        ld8(blk + r * EP_LD + c, f);
-        if (row < m_end) *(uint4*)(out + (size_t)row * w.n + cb + c) = Chunk<elt>::pack(f);
-      }
+    if (cb >= w.n) {  // wave-uniform; n is a multiple of 128
+      stage_wait<0>();
+      return;
     }
+#pragma unroll
+    for (int i = 0; i < TM; ++i)
+#pragma unroll
+      for (int hb = 0; hb < 2; ++hb) {
+        const float* blk = stage_rows(acc, i, hb, smem, p);
+        if (i == 0 && hb == 0) stage_wait<0>();  // the next tile's stage, ahead of the stores
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const int r = q * 4 + (p.lane >> 4), row = m0 + p.wm * WTM + i * 32 + hb * 16 + r;
+          float f[8];
+          ld8(blk + r * EP_LD + c, f);
+          if (row < m_end) put16(out + (size_t)row * w.n + cb + c, Chunk<elt>::pack(f));
+        }
+      }
   }
 };
 
@@ -380,6 +503,7 @@ struct PlainOp {
 // wave's 128 columns are one scale block each.
 template <class E>
 struct DgradActOp {
+  typedef E type;
   typedef typename E::elt elt;
   Rows x;
   Cols w;  // W_down transposed, n = F
@@ -398,19 +522,35 @@ struct DgradActOp {
                                            int nt, uint8_t* smem, float*) const {
     const Pos p = Pos::of();
     const int cb = nt * BN + p.wn * WTN, c = (p.lane & 15) * 8;
+    const int last = m_end - 1, r0 = m0 + p.wm * WTM + (p.lane >> 4);
+    stage_wait<0>();  // the next tile's stage, ahead of the loads and stores
     if (cb >= F) return;  // wave-uniform; F is a multiple of 128
+    // h and the gates of 16 rows, loaded one half tile ahead of their use (a wave's
+    // loads wait for its earlier stores)
+    uint4 gv[2][4], uv[2][4];
+    float gates_[2][4];
+    auto fetch = [&](int s, int at) {
 #pragma unroll
-    for (int i = 0; i < TM; ++i) {
-      const float* blk = stage_rows(acc, i, smem, p);
+      for (int q = 0; q < 4; ++q) {
+        const size_t row = (size_t)min(r0 + at + q * 4, last);
+        gv[s][q] = *(const uint4*)(h + row * 2 * F + cb + c);
+        uv[s][q] = *(const uint4*)(h + row * 2 * F + F + cb + c);
+        gates_[s][q] = x.xrows ? gates[x.xrows[row]] : 1.f;
+      }
+    };
+    fetch(0, 0);
 #pragma unroll
-      for (int q = 0; q < 8; ++q) {
-        const int r = q * 4 + (p.lane >> 4), rr = m0 + p.wm * WTM + i * 32 + r;
-        const size_t row = (size_t)min(rr, m_end - 1);
+    for (int b = 0; b < 2 * TM; ++b) {
+      const float* blk = stage_rows(acc, b >> 1, b & 1, smem, p);
+      if (b + 1 < 2 * TM) fetch((b + 1) & 1, (b + 1) * 16);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int rr = r0 + b * 16 + q * 4;
         float da[8], g[8], u[8], dg[8], du[8], av[8];
-        ld8(blk + r * EP_LD + c, da);
-        Chunk<elt>::unpack(*(const uint4*)(h + row * 2 * F + cb + c), g);
-        Chunk<elt>::unpack(*(const uint4*)(h + row * 2 * F + F + cb + c), u);
-        const float gate = x.xrows ? gates[x.xrows[row]] : 1.f;
+        ld8(blk + (q * 4 + (p.lane >> 4)) * EP_LD + c, da);
+        Chunk<elt>::unpack(gv[b & 1][q], g);
+        Chunk<elt>::unpack(uv[b & 1][q], u);
+        const float gate = gates_[b & 1][q];
 #pragma unroll
         for (int t = 0; t < 8; ++t) {
           const float sg = sigmoid_fast(g[t]), d = da[t] * gate;
@@ -418,14 +558,18 @@ struct DgradActOp {
           du[t] = d * g[t] * sg;
           av[t] = gate * (g[t] * sg) * u[t];
         }
-        const int bg = fp8_scale_byte(lanes_max<16>(amax8(dg)));
-        const int bu = fp8_scale_byte(lanes_max<16>(amax8(du)));
-        if (rr < m_end) {
-          *(uint4*)(dh + row * 2 * F + cb + c) = Chunk<elt>::pack(dg);
-          *(uint4*)(dh + row * 2 * F + F + cb + c) = Chunk<elt>::pack(du);
-          if (ag) *(uint4*)(ag + row * F + cb + c) = Chunk<elt>::pack(av);
-          *(uint2*)(dq + row * 2 * F + cb + c) = quant8(dg, fp8_inv_scale(bg));
-          *(uint2*)(dq + row * 2 * F + F + cb + c) = quant8(du, fp8_inv_scale(bu));
+        const bool ok = rr < m_end;
+        const size_t row = (size_t)rr;
+        if (ok) {
+          put16(dh + row * 2 * F + cb + c, Chunk<elt>::pack(dg));
+          put16(dh + row * 2 * F + F + cb + c, Chunk<elt>::pack(du));
+          if (ag) put16(ag + row * F + cb + c, Chunk<elt>::pack(av));
+        }
+        const int bg = fp8_scale_byte(lanes_max<16>(without_inf(dg, amax8(dg))));
+        const int bu = fp8_scale_byte(lanes_max<16>(without_inf(du, amax8(du))));
+        if (ok) {
+          put8(dq + row * 2 * F + cb + c, quant8(dg, fp8_inv_scale(bg)));
+          put8(dq + row * 2 * F + F + cb + c, quant8(du, fp8_inv_scale(bu)));
           if ((p.lane & 15) == 0) {
             ds[row * ld2F + cb / 128] = (uint8_t)bg;
             ds[row * ld2F + (F + cb) / 128] = (uint8_t)bu;
@@ -436,9 +580,9 @@ struct DgradActOp {
   }
 };
 
-// Row-grouped product over the plan's tiles.  The first stage of the next tile is
-// loaded before the epilogue issues its stores (memory operations of a wave
-// complete in order, so the next main loop need not wait for them).
+// Row-grouped product over the plan's tiles.  The next tile's first stage is copied
+// while a tile's epilogue runs, and ahead of its stores: a wave's memory operations
+// complete in order.
 template <class Op>
 __global__ __launch_bounds__(NT) void fp8_kernel(Op op, const int32_t* __restrict__ offsets,
                                                  const int32_t* __restrict__ tile_offsets,
@@ -453,37 +597,38 @@ __global__ __launch_bounds__(NT) void fp8_kernel(Op op, const int32_t* __restric
   __syncthreads();
   Sched sch(s_to[E_l] * n_tiles);
   if (sch.t >= sch.end) return;  // block-uniform
-  const int tid = threadIdx.x, nk = op.stages(), k1 = nk > 1 ? 1 : 0;
+  const int tid = threadIdx.x, nk = op.stages();
+  // LDS address of this wave's part of buffer 0
+  const uint32_t lds = (uint32_t)__builtin_amdgcn_readfirstlane(
+      (int)((uint32_t)(uintptr_t)(lds_u8_t*)smem + (threadIdx.x >> 6) * 1024u));
   Load la, lb;
   Scales sc;
-  int e, m0, m_end, nt = sch.t % n_tiles;
-  row_tile(s_to, s_off, E_l, sch.t / n_tiles, e, m0, m_end);
-  op.init(e, m0, m_end, nt, la, lb, sc, tid);
-  sc.fetch(0);
-  la.load(0);
-  lb.load(0);
+  int nt, e, m0, m_end;
+  auto locate = [&]() {
+    nt = sch.t % n_tiles;
+    row_tile(s_to, s_off, E_l, sch.t / n_tiles, e, m0, m_end);
+    op.init(e, m0, m_end, nt, la, lb, sc, tid);
+    la.copy(0, lds);
+    lb.copy(0, lds + STAGE);
+    sc.fetch(0);
+  };
+  locate();
+  stage_wait<0>();
   for (;;) {
-    la.store(smem);
-    lb.store(smem + STAGE);
-    la.load(k1);
-    lb.load(k1);
-    __syncthreads();
+    sc.next();
+    la.copy(1, lds + 2 * STAGE, nk > 1);
+    lb.copy(1, lds + 3 * STAGE, nk > 1);
+    __syncthreads();  // every wave's part of stage 0 is here
     f32x16_t acc[TM][TN];
-    mainloop(la, lb, sc, nk, smem, acc);
+    mainloop<Op::type::WIDE>(la, lb, sc, nk, smem, lds, acc);
     const int cm0 = m0, cm_end = m_end, cnt = nt;
     sch.t += sch.step;
     const bool more = sch.t < sch.end;  // block-uniform
-    if (more) {
-      nt = sch.t % n_tiles;
-      row_tile(s_to, s_off, E_l, sch.t / n_tiles, e, m0, m_end);
-      op.init(e, m0, m_end, nt, la, lb, sc, tid);
-      sc.fetch(0);
-      la.load(0);
-      lb.load(0);
-    }
+    if (more) locate();
+    // waits for the next tile's stage 0 and scales ahead of its own stores
     op.epilogue(acc, cm0, cm_end, cnt, smem, s_max);
-    __syncthreads();  // the staging is read before the next tile's stage 0 lands in LDS
     if (!more) break;
+    __syncthreads();  // the staging is read before the next tile's stage 1 lands there
   }
 }
 

@@ -427,15 +427,18 @@ int ffn_dgrad_t(const moe_shape* s, const void* dq, const uint8_t* ds, const int
 
 }  // namespace
 
-// Few rows: up to 256 per expert on average, and E_l F d (mean - 11) <= 1.3e9.  Below it
-// these kernels are faster than the 256 x 256 tiles, whose time hardly falls with the
-// rows; above, the tiles reuse each weight more.  Both sides, forward in us on an
-// MI355X, small against tiles: 128 experts of 2048 x 768 at 16 rows 174 / 189, at 32 297 /
-// 194; 8 experts of 2048 x 768 at 64 36 / 50, at 128 51 / 51; 8 of 2048 x 1408 at 32 46 / 57,
-// at 64 59 / 57; 4 of 640 x 384 at 256 31 / 51.
+// Few rows: up to 256 per expert on average, and E_l F d (mean - 11) up to 1e9 (bf16) or
+// 2.3e9 (fp16, where the tiles multiply at half the rate).  Below it these kernels are faster
+// than the 256 x 256 tiles, whose time hardly falls with the rows; above, the tiles reuse each
+// weight more.  Both sides, forward in us on an MI355X, small against tiles: bf16, 128 experts
+// of 2048 x 768 at 16 rows 190 / 212, at 32 300 / 186; 8 experts of 2048 x 1408 at 32 46 / 51, at 64
+// 59 / 51; 8 of 2048 x 768 at 64 36 / 45, at 128 50 / 46; 4 of 640 x 384 at 256 31 / 46.  fp16, 128
+// experts of 2048 x 768 at 16 193 / 337, at 32 300 / 284; 8 of 2048 x 1408 at 96 75 / 83, at 128
+// 104 / 83.
 bool fp8_small(const moe_shape* s) {
   const int64_t mean = cdiv(s->T * s->K, s->E);
-  return mean <= 256 && s->E_l * s->F * s->d * (mean - 11) <= 1300000000;
+  const int64_t most = s->dtype == MOE_BF16 ? 1000000000 : 2300000000;
+  return mean <= 256 && s->E_l * s->F * s->d * (mean - 11) <= most;
 }
 size_t fp8_small_workspace_bytes(const moe_shape* s) {
   return (size_t)(s->T * s->K * 2 * s->F) * sizeof(float);

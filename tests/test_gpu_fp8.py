@@ -292,6 +292,14 @@ LAYERS = {
     "wide": (9, 16384, 128, 2, 0, 2, 2),
     "wide_ffn": (9, 128, 16384, 2, 0, 2, 2),
     "wide_rows": (300, 2048, 256, 2, 0, 2, 1),
+    # more than 256 rows to an expert, or much work in all: 256 x 256 tiles
+    "tiles_one_block": (520, 128, 128, 2, 0, 2, 2),
+    "tiles_odd_blocks": (300, 640, 384, 1, 0, 1, 1),
+    "tiles_window": (900, 256, 640, 3, 1, 2, 1),
+    "tiles_wide": (300, 16384, 128, 1, 0, 1, 1),
+    "tiles_wide_ffn": (300, 128, 16384, 1, 0, 1, 1),
+    "tiles_few_rows": (170, 2048, 2048, 2, 0, 2, 2),
+    "tiles_past_the_grid": (8192, 128, 256, 64, 0, 64, 8),
 }
 
 
@@ -311,24 +319,27 @@ def test_dgrad(name, dtype, gather):
     L.check_dgrad(L.dgrad())
 
 
-def test_no_local_rows():
+@pytest.mark.parametrize("T,E", [(40, 8), (700, 4)])
+def test_no_local_rows(T, E):
     """Every token is routed outside the window: nothing is written."""
-    L = Layer(40, 128, 128, 8, 4, 2, 2, "bf16", True, only=[0, 1])
+    L = Layer(T, 128, 128, E, 2, 2, 2, "bf16", True, only=[0, 1])
     assert L.N == 0
     L.untouched(**L.forward())
     L.untouched(**L.dgrad())
 
 
-def test_one_expert_has_every_row():
-    L = Layer(700, 128, 128, 8, 0, 8, 1, "bf16", True, only=[5])
-    assert L.off[5] == 0 and L.off[6] == 700
+@pytest.mark.parametrize("T", [700, 2100])
+def test_one_expert_has_every_row(T):
+    L = Layer(T, 128, 128, 8, 0, 8, 1, "bf16", True, only=[5])
+    assert L.off[5] == 0 and L.off[6] == T
     L.check_forward(L.forward())
     L.check_dgrad(L.dgrad())
 
 
-def test_optional_outputs():
+@pytest.mark.parametrize("name", ["ragged_tiles", "tiles_window"])
+def test_optional_outputs(name):
     """h and a left out (serving) change nothing in y; ag left out neither."""
-    L = Layer(*LAYERS["ragged_tiles"], "bf16", True)
+    L = Layer(*LAYERS[name], "bf16", True)
     full = L.forward()
     for h, a in ((False, False), (True, False), (False, True)):
         part = L.forward(h, a)
@@ -338,13 +349,14 @@ def test_optional_outputs():
     assert torch.equal(d["dh"], e["dh"]) and torch.equal(d["dx"], e["dx"])
 
 
-def test_gathered_equals_dispatched():
+@pytest.mark.parametrize("name", ["ragged_tiles", "tiles_window"])
+def test_gathered_equals_dispatched(name):
     """Token rows read through the plan give what the permuted copy gives."""
-    L = Layer(*LAYERS["ragged_tiles"], "bf16", True)
+    L = Layer(*LAYERS[name], "bf16", True)
     f, d = L.forward(), L.dgrad()
     rows = torch.zeros(L.T * L.K, dtype=torch.int64)
     rows[: L.N] = torch.from_numpy(L.pair // L.K)
-    P = Layer(*LAYERS["ragged_tiles"], "bf16", False)
+    P = Layer(*LAYERS[name], "bf16", False)
     P.q = L.q.view(torch.uint8)[rows.cuda()].view(torch.float8_e4m3fn).contiguous()
     P.qs, P.w = L.qs[rows.cuda()].contiguous(), L.w
     assert all(torch.equal(x, y) for x, y in zip(f.values(), P.forward().values()))
@@ -355,9 +367,11 @@ def test_gathered_equals_dispatched():
     assert torch.equal(d["dh"], e["dh"]) and torch.equal(d["dx"], e["dx"])
 
 
-def test_nonfinite_token_stays_in_its_rows():
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("name", ["ragged_tiles", "tiles_odd_blocks"])
+def test_nonfinite_token_stays_in_its_rows(name, dtype):
     """A NaN or infinite activation poisons its own token's outputs only."""
-    L = Layer(*LAYERS["ragged_tiles"], "bf16", True)
+    L = Layer(*LAYERS[name], dtype, True)
     clean = L.forward()
     L.x[7, 3], L.x[9, 100] = float("nan"), float("inf")
     L.q, L.qs = L.quantise(L.x, L.T)
@@ -381,7 +395,22 @@ def test_refuses_another_shapes_weights():
     assert e.value.code == M.MOE_ERR_WORKSPACE
 
 
-@pytest.mark.parametrize("name", ["one_token", "ragged_tiles"])
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("name", ["ragged_tiles", "tiles_odd_blocks"])
+def test_infinite_products_stay_in_their_rows(name, dtype):
+    """Activations whose products pass the type's range: the row's block scales come
+    from its finite values, its infinities become NaN, and other rows keep theirs."""
+    L = Layer(*LAYERS[name], dtype, True)
+    clean = L.forward()
+    L.qs[7, 0] = 254                       # the first block of token 7, times 2^127
+    out = L.forward()
+    bad = torch.from_numpy(np.isin(L.pair // L.K, (7,)))
+    y, c = out["y"][: L.N].float().cpu(), clean["y"][: L.N].float().cpu()
+    assert not torch.isfinite(y[bad]).any()
+    assert torch.equal(y[~bad], c[~bad])
+
+
+@pytest.mark.parametrize("name", ["one_token", "ragged_tiles", "tiles_window"])
 def test_two_streams_and_graph_replays(name):
     """Calls on two streams with a workspace each, and a captured pair of calls
     replayed between eager work, give the eager results bit for bit."""
