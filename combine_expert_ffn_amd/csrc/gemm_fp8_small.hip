@@ -337,10 +337,11 @@ __global__ __launch_bounds__(64 * WAVES) void small_second_kernel(
 
 // Launch shape.  rows: what most experts have at most (the mean of an even routing and two
 // standard deviations of a Poisson count).  S: four groups of 16 columns per block
-// where that leaves a block per CU or more (every block reads, and for the second
-// product quantises, all rows of its expert).  G: as many token groups per pass as
-// the rows fill, fewer where blocks are few, down to one; the passes are spread
-// over the grid's z until there are two blocks per CU.
+// where that and 16 rows per block leave one block per CU or more (every block reads, and
+// for the second product quantises, all of its rows: at 128 rows, 2 experts of 2048 x 2048,
+// 29 us against 71 for the activation gradient's second product).  G: as many token groups
+// per pass as the rows fill, fewer where blocks are few, down to one; the passes are
+// spread over the grid's z until there are two blocks per CU.
 struct Shape {
   int G, S;
   dim3 grid;
@@ -349,10 +350,10 @@ struct Shape {
     const double mean = (double)pairs / (double)s->E;
     const int64_t rows = (int64_t)(mean + 2 * sqrt(mean)) + 1;
     const int64_t slots = pairs < s->E_l ? pairs : s->E_l;
-    S = may_widen && slots * cols / 64 >= 256 ? 4 : 1;
+    S = may_widen && slots * cols / 64 * cdiv(rows, 16) >= 256 ? 4 : 1;
     const int64_t blocks = slots * cols / (16 * S);
     G = rows <= 16 ? 1 : (rows <= 32 ? 2 : 4);
-    while (G > 1 && blocks * cdiv(rows, 16 * G) < 512) G /= 2;
+    while (G > 1 && blocks * cdiv(rows, 16 * G) < (S == 1 ? 512 : 256)) G /= 2;
     int64_t z = cdiv(rows, 16 * G);
     if (z > cdiv(512, blocks)) z = cdiv(512, blocks);
     grid = dim3((unsigned)(cols / (16 * S)), (unsigned)slots, (unsigned)z);
@@ -432,7 +433,7 @@ int ffn_dgrad_t(const moe_shape* s, const void* dq, const uint8_t* ds, const int
 // than the 256 x 256 tiles, whose time hardly falls with the rows; above, the tiles reuse each
 // weight more.  Both sides, forward in us on an MI355X, small against tiles: bf16, 128 experts
 // of 2048 x 768 at 16 rows 190 / 212, at 32 300 / 186; 8 experts of 2048 x 1408 at 32 46 / 51, at 64
-// 59 / 51; 8 of 2048 x 768 at 64 36 / 45, at 128 50 / 46; 4 of 640 x 384 at 256 31 / 46.  fp16, 128
+// 59 / 51; 8 of 2048 x 768 at 64 36 / 45, at 128 50 / 46; 4 of 640 x 384 at 256 24 / 46.  fp16, 128
 // experts of 2048 x 768 at 16 193 / 337, at 32 300 / 284; 8 of 2048 x 1408 at 96 75 / 83, at 128
 // 104 / 83.
 bool fp8_small(const moe_shape* s) {
