@@ -213,9 +213,12 @@ __device__ __forceinline__ void slice(const i32x8_t (&a)[TM], i32x8_t (&an)[TM],
   }
 }
 
+// The reduction over nk stages; stage 0 is in the first buffer, stage 1 is being
+// copied to the second.  idle: the wave's 64 rows lie past the expert's last, so it
+// only copies (2 % of the time at 1024 rows per expert, whose last tiles are half empty).
 template <bool WIDE>
 __device__ __forceinline__ void mainloop(const Load& la, const Load& lb, Scales& sc, int nk,
-                                         uint8_t* smem, uint32_t lds, f32x16_t (&acc)[TM][TN]) {
+                                         uint8_t* smem, uint32_t lds, bool idle, f32x16_t (&acc)[TM][TN]) {
   const Pos w = Pos::of();
 #pragma unroll
   for (int i = 0; i < TM; ++i)
@@ -223,6 +226,18 @@ __device__ __forceinline__ void mainloop(const Load& la, const Load& lb, Scales&
     for (int j = 0; j < TN; ++j)
 #pragma unroll
       for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.f;
+  if (idle) {  // wave-uniform: only its part of the copies, and the barriers
+    for (int kt = 0; kt < nk; ++kt) {
+      const int odd = kt & 1;
+      stage_wait<0>();
+      __syncthreads();
+      la.copy(kt + 2, lds + odd * 2 * STAGE, kt + 2 < nk);
+      lb.copy(kt + 2, lds + odd * 2 * STAGE + STAGE, kt + 2 < nk);
+    }
+    stage_wait<0>();
+    __syncthreads();
+    return;
+  }
   i32x8_t a0[TM], a1[TM], b[TN];
 #pragma unroll
   for (int i = 0; i < TM; ++i) a0[i] = read_frag(smem, w.wm * WTM + i * 32, 0, w.lane);
@@ -620,7 +635,7 @@ __global__ __launch_bounds__(NT) void fp8_kernel(Op op, const int32_t* __restric
     lb.copy(1, lds + 3 * STAGE, nk > 1);
     __syncthreads();  // every wave's part of stage 0 is here
     f32x16_t acc[TM][TN];
-    mainloop<Op::type::WIDE>(la, lb, sc, nk, smem, lds, acc);
+    mainloop<Op::type::WIDE>(la, lb, sc, nk, smem, lds, m0 + Pos::of().wm * WTM >= m_end, acc);
     const int cm0 = m0, cm_end = m_end, cnt = nt;
     sch.t += sch.step;
     const bool more = sch.t < sch.end;  // block-uniform
