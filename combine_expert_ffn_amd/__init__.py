@@ -590,7 +590,8 @@ class AdamWTensors:
     """The tensors of an AdamW step, checked once and kept for many steps.  Each
     is a dict: param (float32, bfloat16 or float16), grad (float32), m and v
     (float32, or float8_e4m3fn with uint8 scales m_s and v_s of
-    ceil(n / 128) elements), and optionally master (float32) and weight_decay."""
+    ceil(n / 128) elements), and optionally master (float32) and weight_decay.
+    What the step writes must not overlap anything else in the list."""
 
     def __init__(self, tensors):
         import torch
@@ -623,6 +624,17 @@ class AdamWTensors:
             self.array[i] = MoeAdamwTensor(
                 n, *[_p(t.get(k)) for k in ("param", "master", "grad", "m", "v", "m_s", "v_s")],
                 s.dtype, int(q8), float(t.get("weight_decay", 0.0)), 0)
+        spans = sorted((x.data_ptr(), x.data_ptr() + x.numel() * x.element_size(),
+                        name != "grad", f"{name} {i}")
+                       for i, t in enumerate(self.tensors)
+                       for name in ("param", "master", "grad", "m", "v", "m_s", "v_s")
+                       if (x := t.get(name)) is not None and x.numel() > 0)
+        end = {False: (0, ""), True: (0, "")}     # the furthest gradient, the furthest written
+        for lo, hi, written, name in spans:
+            for w, (e, other) in end.items():
+                if (written or w) and lo < e:
+                    raise MoeError(MOE_ERR_ARG, f"{fn}: {name} and {other} share memory")
+            end[written] = max(end[written], (hi, name))
 
 
 def moe_adamw(tensors, lr, beta1=0.9, beta2=0.999, eps=1e-8, step=1, grad_scale=1.0,

@@ -187,7 +187,7 @@ int moe_adamw(const moe_adamw_tensor* t, int n, const moe_adamw_hyper* hp, hipSt
   ALIGNED(hp->grad_scale_dev, 4);
   for (int i = 0; i < n; ++i) {
     const moe_adamw_tensor& x = t[i];
-    if (x.n < 0 || x.n >= (1LL << 36))
+    if (x.n < 0 || x.n > (1LL << 34))
       return set_error(MOE_ERR_SHAPE, "%s: tensor %d has %lld elements", __func__, i,
                        (long long)x.n);
     if (x.dtype != MOE_F32 && x.dtype != MOE_BF16 && x.dtype != MOE_F16)

@@ -10,6 +10,9 @@
 // The first product leaves its result in float32; the second quantises the rows
 // as it reads them (each wave its own blocks of 128, in registers), so no block
 // needs another's column maximum.
+// bf16 on an MI355X, forward: one token, 8 of 128 experts of 2048 x 768, 13.9 us (38 MB of
+// weights; two launches and their chains of latencies); 8 rows for each of the 128, 129 us
+// (604 MB, 4.7 TB/s, near the 5.0 of a large copy).
 #include "moe_fp8.h"
 
 #include <math.h>

@@ -612,7 +612,7 @@ int moe_ffn_dgrad_fp8(const moe_shape* s, const void* dq, const uint8_t* ds,
  * each (as above): m holds the first moment, v the square root of the second.
  */
 typedef struct moe_adamw_tensor {
-  int64_t n;          /* elements, 0 <= n < 2^36                               */
+  int64_t n;          /* elements, 0 <= n <= 2^34                              */
   void* param;        /* [n] dtype: the weights, overwritten                   */
   float* master;      /* [n] float32 weights the step updates (param gets them
                          rounded), or NULL: param itself is read and updated   */
@@ -653,7 +653,7 @@ typedef struct moe_adamw_hyper {
  * The hyperparameters are read by the host: a captured graph replays the step
  * number and the learning rate it was captured with.  Empty tensors
  * (and an empty list) are skipped.  Errors: MOE_ERR_NULL, MOE_ERR_SHAPE
- * (n < 0 or a tensor of 2^36 elements or more), MOE_ERR_DTYPE, MOE_ERR_ARG
+ * (n < 0 or a tensor of more than 2^34 elements), MOE_ERR_DTYPE, MOE_ERR_ARG
  * (hyperparameters, alignment, reserved fields, scales given without state8).
  */
 int moe_adamw(const moe_adamw_tensor* t, int n, const moe_adamw_hyper* hp, hipStream_t stream);

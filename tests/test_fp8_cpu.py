@@ -243,6 +243,7 @@ def test_adamw_tensor_sizes():
 
     assert call(-1) == M.MOE_ERR_SHAPE
     assert call(1 << 36) == M.MOE_ERR_SHAPE
+    assert call((1 << 34) + 1) == M.MOE_ERR_SHAPE
     assert call(0) == M.MOE_OK          # nothing to do, nothing launched
     h = M.MoeAdamwHyper(1e-3, 0.9, 0.95, 1e-8, 1, 0, None, 1.0, 0)
     assert M.lib().moe_adamw(None, 0, C.byref(h), None) == M.MOE_OK

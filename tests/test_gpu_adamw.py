@@ -152,6 +152,23 @@ def test_more_tensors_than_one_launch_takes():
         assert (whole[:k] == 0).all() and (whole[k + t["param"].numel():] == 0).all()
 
 
+@pytest.mark.parametrize("bits", [32, 8])
+def test_shared_memory_is_refused(bits):
+    """The same tensor twice, or a buffer inside another, would be a race; one
+    gradient for two tensors is fine."""
+    a, b = make(300, "bf16", bits, True, 1), make(300, "bf16", bits, True, 2)
+    M.AdamWTensors([a, dict(b, grad=a["grad"])])
+    for bad in (dict(a), dict(b, param=a["param"]), dict(b, master=a["grad"]),
+                dict(b, m=a["v"]), dict(b, grad=b["master"]), dict(b, v=b["m"])):
+        with pytest.raises(M.MoeError) as e:
+            M.AdamWTensors([a, bad])
+        assert e.value.code == M.MOE_ERR_ARG
+    flat = torch.zeros(700, dtype=torch.bfloat16, device="cuda")
+    M.AdamWTensors([dict(a, param=flat[:300]), dict(b, param=flat[300:600])])
+    with pytest.raises(M.MoeError):
+        M.AdamWTensors([dict(a, param=flat[:300]), dict(b, param=flat[299:599])])
+
+
 def test_device_gradient_scale():
     a, b = [make(500, "bf16", 8, True, 1)], [make(500, "bf16", 8, True, 1)]
     clip = torch.tensor([0.25], device="cuda")
