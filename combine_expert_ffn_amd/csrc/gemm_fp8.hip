@@ -22,13 +22,14 @@
 //  * outputs are staged through LDS to rows of 128 bytes or more and stored past
 //    L2 (non-temporal), where they would push out the operands that 32 CUs share;
 //  * persistent grid over the dispatch plan's row tiles, one range per XCD.
-// What bounds it: moving operands into LDS.  128 experts of 2048 x 768, 131072 rows,
-// bf16: gate and up 533 us (1.55 PFLOP/s), down 335 (1.23), activation gradient 464 (which
-// also reads h) and 520 (1.59).  With parts left out, gate and up / down: fragment reads and
-// MFMAs alone 280 / 140 us, copies alone 367 / 215, all but the epilogue 404 / 227.  A
-// CU's loads and stores share one queue, so the stores (at the write rate of HBM) add up
-// with the loads.  Two blocks of half the size per CU, four waves of 128 x 128, and rings of
-// 64-byte slices were each slower.
+// What bounds it: moving operands to LDS and results out.  128 experts of 2048 x 768,
+// 131072 rows, bf16: gate and up 508 us (1.62 PFLOP/s), down 284 (1.45), activation gradient
+// 452 (which also reads h) and 459 (1.80).  With parts left out, gate and up / down:
+// fragment reads and MFMAs alone 300 / 168 us, copies alone 319 / 160 (184 / 106 where L2
+// has all), everything but the stores 452 / 225.  A wave's memory operations complete in
+// order, so a tile's stores (at the write rate of HBM) add up with the next one's copies.
+// Slower: two blocks of half the size per CU, four waves of 128 x 128, rings of 64-byte
+// slices, four waves that copy while the other four store.
 #include "moe_fp8.h"
 
 namespace moe {
@@ -78,20 +79,36 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc_of(const void* p) {
 // the chunk that the swizzle puts there.  The copies are inline assembly: the
 // compiler would wait for all of them ahead of every LDS read; here stage_wait()
 // does, once per stage.
+// 1024 bytes of a wave.
+__device__ __forceinline__ void copy_rows(uint32_t off, u32x4_t r, uint32_t at, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
+               :
+               : "s"(lds), "v"(off), "s"(r), "s"(at)
+               : "memory");
+}
+
 struct Load {
+  static constexpr int CH = BM * 128 / (NT * 16), ROWS = BM / CH;
   u32x4_t rsrc;
-  uint32_t off[4];
-  template <class RowOff>
-  __device__ __forceinline__ void init(const void* base, RowOff row_off, int tid) {
+  uint32_t off[CH];
+  __device__ __forceinline__ void set_base(const void* base) {
     const uint64_t p = (uint64_t)base;
     // raw buffer (stride 0); every offset used is a valid byte of the operand
     rsrc = u32x4_t{(uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)p),
                    (uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)(p >> 32)) & 0xffffu,
                    0x7fffffffu, 0x00020000u};
-    const int row = tid >> 3;  // rows 64 apart have the same swizzle
+  }
+  // row r starts at offset(get(r)); get may read memory, for all rows at once
+  template <class Get, class Offset>
+  __device__ __forceinline__ void init(const void* base, Get get, Offset offset, int tid) {
+    set_base(base);
+    const int row = tid >> 3;  // rows 32 apart have the same swizzle
+    int at[CH];
 #pragma unroll
-    for (int c = 0; c < 4; ++c)
-      off[c] = (uint32_t)row_off(c * 64 + row) + (uint32_t)((tid & 7) ^ swz(row)) * 16u;
+    for (int c = 0; c < CH; ++c) at[c] = get(c * ROWS + row);
+#pragma unroll
+    for (int c = 0; c < CH; ++c)
+      off[c] = (uint32_t)offset(at[c]) + (uint32_t)((tid & 7) ^ swz(row)) * 16u;
   }
   // stage kt to the LDS address of this wave's first 1024 bytes; on = false
   // reads nothing (no byte of the buffer is in range; LDS gets zeros), without a
@@ -99,17 +116,36 @@ struct Load {
   __device__ __forceinline__ void copy(int kt, uint32_t lds, bool on = true) const {
     const u32x4_t r = {rsrc[0], rsrc[1], on ? rsrc[2] : 0u, rsrc[3]};
 #pragma unroll
-    for (int c = 0; c < 4; ++c)
-      asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
-                   :
-                   : "s"(lds + c * 64 * 128), "v"(off[c]), "s"(r), "s"(kt * 128)
-                   : "memory");
+    for (int c = 0; c < CH; ++c)
+      copy_rows(off[c], r, (uint32_t)kt * 128u, lds + c * ROWS * 128);
   }
 };
-// Waits until at most N of the wave's memory operations are outstanding.
-template <int N>
+// The same of rows k bytes apart, whose offsets are one vector register and scalars.
+// half: only the first 128 of the 256 rows exist (they are read twice).
+struct LoadRows {
+  static constexpr int CH = BM * 128 / (NT * 16), ROWS = BM / CH;
+  u32x4_t rsrc;
+  uint32_t off, step, upper;
+  __device__ __forceinline__ void init(const uint8_t* base, int k, bool half, int tid) {
+    Load l;
+    l.set_base(base);
+    rsrc = l.rsrc;
+    off = (uint32_t)((tid >> 3) * k) + (uint32_t)((tid & 7) ^ swz(tid >> 3)) * 16u;
+    step = (uint32_t)__builtin_amdgcn_readfirstlane(ROWS * k);
+    upper = (uint32_t)__builtin_amdgcn_readfirstlane(half ? 0 : 128 * k);
+  }
+  __device__ __forceinline__ void copy(int kt, uint32_t lds, bool on = true) const {
+    const u32x4_t r = {rsrc[0], rsrc[1], on ? rsrc[2] : 0u, rsrc[3]};
+#pragma unroll
+    for (int c = 0; c < CH; ++c)
+      copy_rows(off, r,
+                       (uint32_t)kt * 128u + (c % (CH / 2)) * step + (c / (CH / 2)) * upper,
+                       lds + c * ROWS * 128);
+  }
+};
+// Waits for the wave's memory operations.
 __device__ __forceinline__ void stage_wait() {
-  asm volatile("s_waitcnt vmcnt(%0)" : : "n"(N) : "memory");
+  asm volatile("s_waitcnt vmcnt(0)" : : : "memory");
 }
 
 // Scale bytes of four stages at a time: of the wave's rows (one per lane and
@@ -118,17 +154,36 @@ struct Scales {
   __amdgpu_buffer_rsrc_t ra, rb;
   uint32_t oa[TM], ob[2];
   uint32_t a[TM], b[2], an[TM], bn[2];
-  __device__ __forceinline__ void fetch(int kt) {
+  __device__ __forceinline__ void fetch(int k, uint32_t (&ta)[TM], uint32_t (&tb)[2]) const {
 #pragma unroll
-    for (int i = 0; i < TM; ++i) an[i] = __builtin_amdgcn_raw_buffer_load_b32(ra, (int)oa[i], kt, 0);
+    for (int i = 0; i < TM; ++i) ta[i] = __builtin_amdgcn_raw_buffer_load_b32(ra, (int)oa[i], k, 0);
 #pragma unroll
-    for (int h = 0; h < 2; ++h) bn[h] = __builtin_amdgcn_raw_buffer_load_b32(rb, (int)ob[h], kt, 0);
+    for (int h = 0; h < 2; ++h) tb[h] = __builtin_amdgcn_raw_buffer_load_b32(rb, (int)ob[h], k, 0);
+  }
+  // the group of block k now, and the one after it
+  __device__ __forceinline__ void start(int k, int nk) {
+    fetch(k & ~3, a, b);
+    fetch((k | 3) + 1 < nk ? (k | 3) + 1 : 0, an, bn);
+  }
+  // both are here
+  __device__ __forceinline__ void arrived() {
+#pragma unroll
+    for (int i = 0; i < TM; ++i) asm volatile("" : "+v"(a[i]), "+v"(an[i]));
+#pragma unroll
+    for (int h = 0; h < 2; ++h) asm volatile("" : "+v"(b[h]), "+v"(bn[h]));
+  }
+  // A move that the compiler cannot fold: else it moves the values of the next
+  // fetch instead, and waits for them.
+  static __device__ __forceinline__ uint32_t moved(uint32_t v) {
+    uint32_t r;
+    asm volatile("v_mov_b32 %0, %1" : "=v"(r) : "v"(v));
+    return r;
   }
   __device__ __forceinline__ void next() {
 #pragma unroll
-    for (int i = 0; i < TM; ++i) a[i] = an[i];
-    b[0] = bn[0];
-    b[1] = bn[1];
+    for (int i = 0; i < TM; ++i) a[i] = moved(an[i]);
+    b[0] = moved(bn[0]);
+    b[1] = moved(bn[1]);
   }
 };
 
@@ -217,12 +272,16 @@ __device__ __forceinline__ void slice(const i32x8_t (&a)[TM], i32x8_t (&an)[TM],
   }
 }
 
-// The reduction over nk stages; stage 0 is in the first buffer, stage 1 is being
-// copied to the second.  idle: the wave's 64 rows lie past the expert's last, so it
+// The block of the reduction after k, around its end.
+__device__ __forceinline__ int after(int k, int nk) { return k + 1 < nk ? k + 1 : 0; }
+
+// The reduction over nk blocks from block k0 around; the first stage is in the first
+// buffer, the second is being copied to the other.  idle: the wave's 64 rows lie past the expert's last, so it
 // only copies (2 % of the time at 1024 rows per expert, whose last tiles are half empty).
-template <bool WIDE>
-__device__ __forceinline__ void mainloop(const Load& la, const Load& lb, Scales& sc, int nk,
-                                         uint8_t* smem, uint32_t lds, bool idle, f32x16_t (&acc)[TM][TN]) {
+template <bool WIDE, class LoadB>
+__device__ __forceinline__ void mainloop(const Load& la, const LoadB& lb, Scales& sc,
+                                         int nk, int k0, uint8_t* smem, uint32_t lds,
+                                         bool idle, f32x16_t (&acc)[TM][TN]) {
   const Pos w = Pos::of();
 #pragma unroll
   for (int i = 0; i < TM; ++i)
@@ -230,15 +289,18 @@ __device__ __forceinline__ void mainloop(const Load& la, const Load& lb, Scales&
     for (int j = 0; j < TN; ++j)
 #pragma unroll
       for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.f;
+  int kb = k0;                      // the stage's block of the reduction
+  int kc = after(after(k0, nk), nk);  // the block that is copied next
   if (idle) {  // wave-uniform: only its part of the copies, and the barriers
     for (int kt = 0; kt < nk; ++kt) {
       const int odd = kt & 1;
-      stage_wait<0>();
+      stage_wait();
       __syncthreads();
-      la.copy(kt + 2, lds + odd * 2 * STAGE, kt + 2 < nk);
-      lb.copy(kt + 2, lds + odd * 2 * STAGE + STAGE, kt + 2 < nk);
+      la.copy(kc, lds + odd * 2 * STAGE, kt + 2 < nk);
+      lb.copy(kc, lds + odd * 2 * STAGE + STAGE, kt + 2 < nk);
+      kc = after(kc, nk);
     }
-    stage_wait<0>();
+    stage_wait();
     __syncthreads();
     return;
   }
@@ -247,30 +309,36 @@ __device__ __forceinline__ void mainloop(const Load& la, const Load& lb, Scales&
   for (int i = 0; i < TM; ++i) a0[i] = read_frag(smem, w.wm * WTM + i * 32, 0, w.lane);
 #pragma unroll
   for (int j = 0; j < TN; ++j) b[j] = read_frag(smem + STAGE, w.wn * WTN + j * 32, 0, w.lane);
-  for (int kt = 0; kt < nk; ++kt) {
-    const int odd = kt & 1;
-    const uint8_t* cur = smem + odd * 2 * STAGE;
-    const uint8_t* nxt = smem + (odd ^ 1) * 2 * STAGE;
-    if ((kt & 3) == 0) {
-      if (kt > 0) sc.next();
-      sc.fetch(min(kt + 4, (nk - 1) & ~3));
-    }
-    const int sh = (kt & 3) * 8;
-    uint32_t sa[TM], sb[2];
+  for (int kt = 0; kt < nk;) {
+    // the stages that share a register of scale bytes
+    const int end = min(kt + min(4 - (kb & 3), nk - kb), nk);
+    for (; kt < end; ++kt, ++kb) {
+      const int odd = kt & 1;
+      const uint8_t* cur = smem + odd * 2 * STAGE;
+      const uint8_t* nxt = smem + (odd ^ 1) * 2 * STAGE;
+      const int sh = (kb & 3) * 8;
+      uint32_t sa[TM], sb[2];
 #pragma unroll
-    for (int i = 0; i < TM; ++i) sa[i] = sc.a[i] >> sh;
-    sb[0] = sc.b[0] >> sh;
-    sb[1] = sc.b[1] >> sh;
+      for (int i = 0; i < TM; ++i) sa[i] = sc.a[i] >> sh;
+      sb[0] = sc.b[0] >> sh;
+      sb[1] = sc.b[1] >> sh;
+      __builtin_amdgcn_sched_barrier(0);
+      slice<WIDE>(a0, a1, b, sa, sb, acc, cur, 1, w);
+      stage_wait();
+      __syncthreads();
+      la.copy(kc, lds + odd * 2 * STAGE, kt + 2 < nk);
+      lb.copy(kc, lds + odd * 2 * STAGE + STAGE, kt + 2 < nk);
+      kc = after(kc, nk);
+      __builtin_amdgcn_sched_barrier(0);
+      slice<WIDE>(a1, a0, b, sa, sb, acc, nxt, 0, w);
+    }
+    if (kb == nk) kb = 0;
+    sc.next();
     __builtin_amdgcn_sched_barrier(0);
-    slice<WIDE>(a0, a1, b, sa, sb, acc, cur, 1, w);
-    stage_wait<0>();
-    __syncthreads();
-    la.copy(kt + 2, lds + odd * 2 * STAGE, kt + 2 < nk);
-    lb.copy(kt + 2, lds + odd * 2 * STAGE + STAGE, kt + 2 < nk);
+    sc.fetch((kb | 3) + 1 < nk ? (kb | 3) + 1 : 0, sc.an, sc.bn);
     __builtin_amdgcn_sched_barrier(0);
-    slice<WIDE>(a1, a0, b, sa, sb, acc, nxt, 0, w);
   }
-  stage_wait<0>();  // the copies past the last stage write zeros to LDS
+  stage_wait();  // the copies past the last stage write zeros to LDS
   __syncthreads();
 }
 
@@ -316,13 +384,17 @@ struct Rows {
     const Pos w = Pos::of();
     const int sr = w.wm * WTM + (w.lane & 31);
     if (xrows) {  // block-uniform
-      la.init(q, [&](int r) { return xrows[min(m0 + r, m_end - 1)] / K * k; }, tid);
+      int sp[TM];
+#pragma unroll
+      for (int i = 0; i < TM; ++i) sp[i] = xrows[min(m0 + sr + i * 32, m_end - 1)];
+      la.init(q, [&](int r) { return xrows[min(m0 + r, m_end - 1)]; },
+              [&](int pair) { return pair / K * k; }, tid);
       sc.ra = rsrc_of(s);
 #pragma unroll
-      for (int i = 0; i < TM; ++i)
-        sc.oa[i] = (uint32_t)(xrows[min(m0 + sr + i * 32, m_end - 1)] / K) * (uint32_t)ld;
+      for (int i = 0; i < TM; ++i) sc.oa[i] = (uint32_t)(sp[i] / K) * (uint32_t)ld;
     } else {
-      la.init(q + (size_t)m0 * k, [&](int r) { return (min(m0 + r, m_end - 1) - m0) * k; }, tid);
+      la.init(q + (size_t)m0 * k, [&](int r) { return (min(m0 + r, m_end - 1) - m0) * k; },
+              [](int at) { return at; }, tid);
       sc.ra = rsrc_of(s + (size_t)m0 * ld);
 #pragma unroll
       for (int i = 0; i < TM; ++i)
@@ -337,9 +409,9 @@ struct Cols {
   const uint8_t* s;
   int n, k, ld;
   // plain columns nt * 256 + ..., clamped to the matrix
-  __device__ __forceinline__ void init(int e, int nt, Load& lb, Scales& sc, int tid) const {
+  __device__ __forceinline__ void init(int e, int nt, LoadRows& lb, Scales& sc, int tid) const {
     const Pos w = Pos::of();
-    lb.init(q + (size_t)e * n * k, [&](int c) { return min(nt * BN + c, n - 1) * k; }, tid);
+    lb.init(q + ((size_t)e * n + (size_t)nt * BN) * k, k, nt * BN + 128 >= n, tid);
     sc.rb = rsrc_of(s + (size_t)e * (n / 128) * ld);
     sc.ob[0] = sc.ob[1] = (uint32_t)(min(nt * 2 + w.wn, n / 128 - 1) * ld);
   }
@@ -422,19 +494,23 @@ struct GateUpOp {
   uint8_t *aq, *as;
   int F, ldF;
   __device__ __forceinline__ int stages() const { return x.k / 128; }
-  __device__ __forceinline__ void init(int e, int m0, int m_end, int nt, Load& la, Load& lb,
-                                       Scales& sc, int tid) const {
+  typedef Load LoadB;
+  __device__ __forceinline__ void init(int e, int m0, int m_end, int nt, Load& la,
+                                       LoadB& lb, Scales& sc, int tid) const {
     x.init(m0, m_end, la, sc, tid);
-    lb.init(w.q + (size_t)e * w.n * w.k, [&](int c) {
-      const int j = nt * 128 + (c >> 7) * 64 + (c & 63);
-      return (((c >> 6) & 1) * F + j) * w.k;
-    }, tid);
+    lb.init(w.q + (size_t)e * w.n * w.k,
+            [&](int c) {
+              const int j = nt * 128 + (c >> 7) * 64 + (c & 63);
+              return (((c >> 6) & 1) * F + j) * w.k;
+            },
+            [](int at) { return at; }, tid);
     sc.rb = rsrc_of(w.s + (size_t)e * (w.n / 128) * w.ld);
     sc.ob[0] = (uint32_t)(nt * w.ld);
     sc.ob[1] = (uint32_t)((F / 128 + nt) * w.ld);
   }
+  template <class Arrived>
   __device__ __forceinline__ void epilogue(const f32x16_t (&acc)[TM][TN], int m0, int m_end,
-                                           int nt, uint8_t* smem, float* s_max) const {
+                                           int nt, uint8_t* smem, float* s_max, Arrived arrived) const {
     const Pos p = Pos::of();
     const int c = (p.lane & 7) * 8, j0 = nt * 128 + p.wn * 64 + c;
     float av[TM][4][8];
@@ -450,7 +526,7 @@ struct GateUpOp {
         ld8(blk + r * EP_LD + 64 + c, u);
 #pragma unroll
         for (int t = 0; t < 8; ++t) av[i][q][t] = silu_fast(g[t]) * u[t];
-        if (i == 0 && q == 0) stage_wait<0>();  // the next tile's stage, ahead of the stores
+        if (i == 0 && q == 0) arrived();
         if (m0 + tr < m_end) {
           const size_t row = (size_t)(m0 + tr);
           if (h) {
@@ -488,25 +564,24 @@ struct PlainOp {
   Cols w;
   elt* out;  // [rows][w.n]
   __device__ __forceinline__ int stages() const { return x.k / 128; }
-  __device__ __forceinline__ void init(int e, int m0, int m_end, int nt, Load& la, Load& lb,
-                                       Scales& sc, int tid) const {
+  typedef LoadRows LoadB;
+  __device__ __forceinline__ void init(int e, int m0, int m_end, int nt, Load& la,
+                                       LoadB& lb, Scales& sc, int tid) const {
     x.init(m0, m_end, la, sc, tid);
     w.init(e, nt, lb, sc, tid);
   }
+  template <class Arrived>
   __device__ __forceinline__ void epilogue(const f32x16_t (&acc)[TM][TN], int m0, int m_end,
-                                           int nt, uint8_t* smem, float*) const {
+                                           int nt, uint8_t* smem, float*, Arrived arrived) const {
     const Pos p = Pos::of();
     const int cb = nt * BN + p.wn * WTN, c = (p.lane & 15) * 8;
-    if (cb >= w.n) {  // wave-uniform; n is a multiple of 128
-      stage_wait<0>();
-      return;
-    }
 #pragma unroll
     for (int i = 0; i < TM; ++i)
 #pragma unroll
       for (int hb = 0; hb < 2; ++hb) {
         const float* blk = stage_rows(acc, i, hb, smem, p);
-        if (i == 0 && hb == 0) stage_wait<0>();  // the next tile's stage, ahead of the stores
+        if (i + hb == 0) arrived();
+        if (cb >= w.n) continue;  // wave-uniform; n is a multiple of 128
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
           const int r = q * 4 + (p.lane >> 4), row = m0 + p.wm * WTM + i * 32 + hb * 16 + r;
@@ -532,17 +607,19 @@ struct DgradActOp {
   uint8_t *dq, *ds;  // [rows][2F], [rows][ld2F]
   int F, ld2F;
   __device__ __forceinline__ int stages() const { return x.k / 128; }
-  __device__ __forceinline__ void init(int e, int m0, int m_end, int nt, Load& la, Load& lb,
-                                       Scales& sc, int tid) const {
+  typedef LoadRows LoadB;
+  __device__ __forceinline__ void init(int e, int m0, int m_end, int nt, Load& la,
+                                       LoadB& lb, Scales& sc, int tid) const {
     x.init(m0, m_end, la, sc, tid);
     w.init(e, nt, lb, sc, tid);
   }
+  template <class Arrived>
   __device__ __forceinline__ void epilogue(const f32x16_t (&acc)[TM][TN], int m0, int m_end,
-                                           int nt, uint8_t* smem, float*) const {
+                                           int nt, uint8_t* smem, float*, Arrived arrived) const {
     const Pos p = Pos::of();
     const int cb = nt * BN + p.wn * WTN, c = (p.lane & 15) * 8;
     const int last = m_end - 1, r0 = m0 + p.wm * WTM + (p.lane >> 4);
-    stage_wait<0>();  // the next tile's stage, ahead of the loads and stores
+    arrived();
     if (cb >= F) return;  // wave-uniform; F is a multiple of 128
     // h and the gates of 16 rows, loaded one half tile ahead of their use (a wave's
     // loads wait for its earlier stores)
@@ -599,6 +676,18 @@ struct DgradActOp {
   }
 };
 
+// The 32 CUs of an XCD work on consecutive tiles: n_tiles column tiles of each row
+// tile.  In step, all that share an operand panel ask for its lines at once and wait
+// for memory together; started at different blocks of the reduction, one fetches
+// a line and the others find it in L2.  That needs the panels of 32 tiles to stay there
+// (4 MB; 32 KB per panel and block): 128 experts of 2048 x 768, 131072 rows, down (2.3 MB) 335 ->
+// 288 us, input gradient (4.7 MB) 520 -> 461; gate and up (6 MB) 530 -> 532, activation
+// gradient (7 MB) 459 -> 471.
+__device__ __forceinline__ bool panels_fit(int n_tiles, int nk) {
+  const int cols = n_tiles < 32 ? n_tiles : 32;
+  return (cols + (31 + cols) / cols) * nk <= 160;
+}
+
 // Row-grouped product over the plan's tiles.  The next tile's first stage is copied
 // while a tile's epilogue runs, and ahead of its stores: a wave's memory operations
 // complete in order.
@@ -617,35 +706,41 @@ __global__ __launch_bounds__(NT) void fp8_kernel(Op op, const int32_t* __restric
   Sched sch(s_to[E_l] * n_tiles);
   if (sch.t >= sch.end) return;  // block-uniform
   const int tid = threadIdx.x, nk = op.stages();
+  const bool rotate = panels_fit(n_tiles, nk);
   // LDS address of this wave's part of buffer 0
   const uint32_t lds = (uint32_t)__builtin_amdgcn_readfirstlane(
       (int)((uint32_t)(uintptr_t)(lds_u8_t*)smem + (threadIdx.x >> 6) * 1024u));
-  Load la, lb;
+  Load la;
+  typename Op::LoadB lb;
   Scales sc;
-  int nt, e, m0, m_end;
+  int nt, e, m0, m_end, k0;
   auto locate = [&]() {
     nt = sch.t % n_tiles;
     row_tile(s_to, s_off, E_l, sch.t / n_tiles, e, m0, m_end);
     op.init(e, m0, m_end, nt, la, lb, sc, tid);
-    la.copy(0, lds);
-    lb.copy(0, lds + STAGE);
-    sc.fetch(0);
+    k0 = rotate ? (int)(blockIdx.x / 8) % nk : 0;
+    la.copy(k0, lds);
+    lb.copy(k0, lds + STAGE);
+    sc.start(k0, nk);
+  };
+  // The next tile's first stage and scales are here, ahead of this one's stores.
+  auto arrived = [&]() {
+    stage_wait();
+    sc.arrived();
   };
   locate();
-  stage_wait<0>();
+  arrived();
   for (;;) {
-    sc.next();
-    la.copy(1, lds + 2 * STAGE, nk > 1);
-    lb.copy(1, lds + 3 * STAGE, nk > 1);
+    la.copy(after(k0, nk), lds + 2 * STAGE, nk > 1);
+    lb.copy(after(k0, nk), lds + 3 * STAGE, nk > 1);
     __syncthreads();  // every wave's part of stage 0 is here
     f32x16_t acc[TM][TN];
-    mainloop<Op::type::WIDE>(la, lb, sc, nk, smem, lds, m0 + Pos::of().wm * WTM >= m_end, acc);
+    mainloop<Op::type::WIDE>(la, lb, sc, nk, k0, smem, lds, m0 + Pos::of().wm * WTM >= m_end, acc);
     const int cm0 = m0, cm_end = m_end, cnt = nt;
     sch.t += sch.step;
     const bool more = sch.t < sch.end;  // block-uniform
     if (more) locate();
-    // waits for the next tile's stage 0 and scales ahead of its own stores
-    op.epilogue(acc, cm0, cm_end, cnt, smem, s_max);
+    op.epilogue(acc, cm0, cm_end, cnt, smem, s_max, arrived);
     if (!more) break;
     __syncthreads();  // the staging is read before the next tile's stage 1 lands there
   }
