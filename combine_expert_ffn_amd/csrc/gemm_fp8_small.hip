@@ -431,17 +431,18 @@ int ffn_dgrad_t(const moe_shape* s, const void* dq, const uint8_t* ds, const int
 
 }  // namespace
 
-// Few rows: up to 256 per expert on average, and E_l F d (mean - 11) up to 1e9 (bf16) or
-// 2.3e9 (fp16, where the tiles multiply at half the rate).  Below it these kernels are faster
-// than the 256 x 256 tiles, whose time hardly falls with the rows; above, the tiles reuse each
-// weight more.  Both sides, forward in us on an MI355X, small against tiles: bf16, 128 experts
-// of 2048 x 768 at 16 rows 190 / 212, at 32 300 / 186; 8 experts of 2048 x 1408 at 32 46 / 51, at 64
-// 59 / 51; 8 of 2048 x 768 at 64 36 / 45, at 128 50 / 46; 4 of 640 x 384 at 256 24 / 46.  fp16, 128
-// experts of 2048 x 768 at 16 193 / 337, at 32 300 / 284; 8 of 2048 x 1408 at 96 75 / 83, at 128
-// 104 / 83.
-bool fp8_small(const moe_shape* s) {
+// Few rows: up to 256 per expert on average, and E_l F d (mean - 11) up to 0.8e9 for the
+// forward and 1.3e9 for the gradient in bf16, 1.4e9 and 1.9e9 in fp16 (where the tiles multiply
+// at half the rate).  Below it these kernels are faster than the 256 x 256 tiles, whose time
+// hardly falls with the rows; above, the tiles reuse each weight more.  Both sides in us on
+// an MI355X, small against tiles, forward and gradient: bf16, 128 experts of 2048 x 768 at 16
+// rows 174 / 171 and 187 / 202, at 32 297 / 171 and 347 / 203; 8 experts of 2048 x 1408 at 32
+// 47 / 44 and 55 / 67, at 64 59 / 44 and 69 / 68; 8 of 2048 x 768 at 64 36 / 38 and 39 / 56, at
+// 128 50 / 40 and 59 / 58; 4 of 640 x 384 at 256 24 / 32 and 28 / 49.  fp16: 8 of 2048 x 1408 at
+// 64 59 / 59 and 69 / 86, at 128 104 / 60 and 121 / 89.
+bool fp8_small(const moe_shape* s, bool dgrad) {
   const int64_t mean = cdiv(s->T * s->K, s->E);
-  const int64_t most = s->dtype == MOE_BF16 ? 1000000000 : 2300000000;
+  const int64_t most = (s->dtype == MOE_BF16 ? 800000000 : 1400000000) + (dgrad ? 500000000 : 0);
   return mean <= 256 && s->E_l * s->F * s->d * (mean - 11) <= most;
 }
 size_t fp8_small_workspace_bytes(const moe_shape* s) {

@@ -67,7 +67,7 @@ int launch_ffn_dgrad_fp8(const moe_shape* s, const void* dq, const uint8_t* ds,
                          const moe_fp8_weights* w, void* dh, void* dxp, void* ag, void* ws,
                          hipStream_t st);
 // The same for few rows per expert (gemm_fp8_small.hip), and the rule that takes it.
-bool fp8_small(const moe_shape* s);
+bool fp8_small(const moe_shape* s, bool dgrad);
 size_t fp8_small_workspace_bytes(const moe_shape* s);
 int launch_ffn_fwd_fp8_small(const moe_shape* s, const void* xq, const uint8_t* xs,
                              const int32_t* xrows, const int32_t* offsets,

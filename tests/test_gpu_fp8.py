@@ -298,7 +298,9 @@ LAYERS = {
     "tiles_window": (900, 256, 640, 3, 1, 2, 1),
     "tiles_wide": (300, 16384, 128, 1, 0, 1, 1),
     "tiles_wide_ffn": (300, 128, 16384, 1, 0, 1, 1),
-    "tiles_few_rows": (170, 2048, 2048, 2, 0, 2, 2),
+    "tiles_few_rows": (250, 2048, 2048, 2, 0, 2, 2),
+    "tiles_forward_only": (120, 2048, 2048, 2, 0, 2, 2),
+    "tiles_halves": (1100, 128, 1408, 8, 0, 8, 4),
     "tiles_past_the_grid": (8192, 128, 256, 64, 0, 64, 8),
 }
 
