@@ -344,7 +344,7 @@ __global__ __launch_bounds__(64 * WAVES) void small_second_kernel(
 // for the second product quantises, all of its rows: at 128 rows, 2 experts of 2048 x 2048,
 // 29 us against 71 for the activation gradient's second product).  G: as many token groups
 // per pass as the rows fill, fewer where blocks are few, down to one; the passes are
-// spread over the grid's z until there are two blocks per CU.
+// spread over the grid's z until there are four blocks per CU.
 struct Shape {
   int G, S;
   dim3 grid;
@@ -358,7 +358,7 @@ struct Shape {
     G = rows <= 16 ? 1 : (rows <= 32 ? 2 : 4);
     while (G > 1 && blocks * cdiv(rows, 16 * G) < (S == 1 ? 512 : 256)) G /= 2;
     int64_t z = cdiv(rows, 16 * G);
-    if (z > cdiv(512, blocks)) z = cdiv(512, blocks);
+    if (z > cdiv(1024, blocks)) z = cdiv(1024, blocks);
     grid = dim3((unsigned)(cols / (16 * S)), (unsigned)slots, (unsigned)z);
   }
 };
