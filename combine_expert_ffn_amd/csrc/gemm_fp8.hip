@@ -73,13 +73,11 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc_of(const void* p) {
   return __builtin_amdgcn_make_buffer_rsrc((void*)p, (short)0, 0x7fffffff, 0x00020000);
 }
 
-// One operand's 256 rows, copied straight to LDS (no registers in between): 4
-// instructions per wave and stage, each writing 1024 consecutive bytes = 8 tile
-// rows; lane l's 16 bytes land at chunk l % 8 of row l / 8, so the lane reads
-// the chunk that the swizzle puts there.  The copies are inline assembly: the
-// compiler would wait for all of them ahead of every LDS read; here stage_wait()
-// does, once per stage.
-// 1024 bytes of a wave.
+// A wave's copy of 8 tile rows straight to LDS (no registers in between): 1024
+// consecutive bytes there; lane l's 16 bytes land at chunk l % 8 of row l / 8, so the
+// lane reads the chunk that the swizzle puts there.  Inline assembly, since the
+// compiler would wait for all copies ahead of every LDS read; stage_wait() does, once
+// per stage.
 __device__ __forceinline__ void copy_rows(uint32_t off, u32x4_t r, uint32_t at, uint32_t lds) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
                :
@@ -87,6 +85,7 @@ __device__ __forceinline__ void copy_rows(uint32_t off, u32x4_t r, uint32_t at, 
                : "memory");
 }
 
+// One operand's 256 rows: 4 copies per wave and stage, 64 rows apart.
 struct Load {
   static constexpr int CH = BM * 128 / (NT * 16), ROWS = BM / CH;
   u32x4_t rsrc;
@@ -102,7 +101,7 @@ struct Load {
   template <class Get, class Offset>
   __device__ __forceinline__ void init(const void* base, Get get, Offset offset, int tid) {
     set_base(base);
-    const int row = tid >> 3;  // rows 32 apart have the same swizzle
+    const int row = tid >> 3;  // rows 64 apart have the same swizzle
     int at[CH];
 #pragma unroll
     for (int c = 0; c < CH; ++c) at[c] = get(c * ROWS + row);
@@ -110,10 +109,10 @@ struct Load {
     for (int c = 0; c < CH; ++c)
       off[c] = (uint32_t)offset(at[c]) + (uint32_t)((tid & 7) ^ swz(row)) * 16u;
   }
-  // stage kt to the LDS address of this wave's first 1024 bytes; on = false
+  // block kt to the LDS address of this wave's first 1024 bytes; on = false
   // reads nothing (no byte of the buffer is in range; LDS gets zeros), without a
-  // branch, past which the compiler would sink the MFMAs before it
-  // (below = false: nor for the lower half of the rows)
+  // branch, past which the compiler would sink the MFMAs before it; below = false
+  // reads nothing for the lower half of the rows
   __device__ __forceinline__ void copy(int kt, uint32_t lds, bool on = true,
                                        bool below = true) const {
     const u32x4_t r = {rsrc[0], rsrc[1], on ? rsrc[2] : 0u, rsrc[3]};
@@ -141,11 +140,11 @@ struct LoadRows {
     const u32x4_t r = {rsrc[0], rsrc[1], on ? rsrc[2] : 0u, rsrc[3]};
 #pragma unroll
     for (int c = 0; c < CH; ++c)
-      copy_rows(off, r,
-                       (uint32_t)kt * 128u + (c % (CH / 2)) * step + (c / (CH / 2)) * upper,
-                       lds + c * ROWS * 128);
+      copy_rows(off, r, (uint32_t)kt * 128u + (c % (CH / 2)) * step + (c / (CH / 2)) * upper,
+                lds + c * ROWS * 128);
   }
 };
+
 // Waits for the wave's memory operations.
 __device__ __forceinline__ void stage_wait() {
   asm volatile("s_waitcnt vmcnt(0)" : : : "memory");
@@ -279,12 +278,13 @@ __device__ __forceinline__ void slice(const i32x8_t (&a)[TM], i32x8_t (&an)[TM],
 __device__ __forceinline__ int after(int k, int nk) { return k + 1 < nk ? k + 1 : 0; }
 
 // The reduction over nk blocks from block k0 around; the first stage is in the first
-// buffer, the second is being copied to the other.  idle: the wave's 64 rows lie past the expert's last, so it
-// only copies (2 % of the time at 1024 rows per expert, whose last tiles are half empty).
+// buffer, the second is being copied to the other.  below: the tile has rows past
+// the first 128.  idle: the wave's 64 rows lie past the tile's last, so it only copies (2 %
+// of the time at 1024 rows per expert, whose last tiles are half empty).
 template <bool WIDE, class LoadB>
-__device__ __forceinline__ void mainloop(const Load& la, const LoadB& lb, Scales& sc,
-                                         int nk, int k0, uint8_t* smem, uint32_t lds,
-                                         bool below, bool idle, f32x16_t (&acc)[TM][TN]) {
+__device__ __forceinline__ void mainloop(const Load& la, const LoadB& lb, Scales& sc, int nk,
+                                         int k0, uint8_t* smem, uint32_t lds, bool below, bool idle,
+                                         f32x16_t (&acc)[TM][TN]) {
   const Pos w = Pos::of();
 #pragma unroll
   for (int i = 0; i < TM; ++i)
@@ -292,7 +292,7 @@ __device__ __forceinline__ void mainloop(const Load& la, const LoadB& lb, Scales
     for (int j = 0; j < TN; ++j)
 #pragma unroll
       for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.f;
-  int kb = k0;                      // the stage's block of the reduction
+  int kb = k0;                        // the stage's block of the reduction
   int kc = after(after(k0, nk), nk);  // the block that is copied next
   if (idle) {  // wave-uniform: only its part of the copies, and the barriers
     for (int kt = 0; kt < nk; ++kt) {
@@ -425,7 +425,7 @@ struct Cols {
   const uint8_t* q;
   const uint8_t* s;
   int n, k, ld;
-  // plain columns nt * 256 + ..., clamped to the matrix
+  // columns nt * 256 ..+255; n is a multiple of 128, so the last tile may be half
   __device__ __forceinline__ void init(int e, int nt, LoadRows& lb, Scales& sc, int tid) const {
     const Pos w = Pos::of();
     lb.init(q + ((size_t)e * n + (size_t)nt * BN) * k, k, nt * BN + 128 >= n, tid);
@@ -512,8 +512,8 @@ struct GateUpOp {
   int F, ldF;
   __device__ __forceinline__ int stages() const { return x.k / 128; }
   typedef Load LoadB;
-  __device__ __forceinline__ void init(int e, int m0, int m_end, int nt, Load& la,
-                                       LoadB& lb, Scales& sc, int tid) const {
+  __device__ __forceinline__ void init(int e, int m0, int m_end, int nt, Load& la, LoadB& lb,
+                                       Scales& sc, int tid) const {
     x.init(m0, m_end, la, sc, tid);
     lb.init(w.q + (size_t)e * w.n * w.k,
             [&](int c) {
@@ -527,7 +527,8 @@ struct GateUpOp {
   }
   template <class Arrived>
   __device__ __forceinline__ void epilogue(const f32x16_t (&acc)[TM][TN], int m0, int m_end,
-                                           int nt, uint8_t* smem, float* s_max, Arrived arrived) const {
+                                           int nt, uint8_t* smem, float* s_max,
+                                           Arrived arrived) const {
     const Pos p = Pos::of();
     const int c = (p.lane & 7) * 8, j0 = nt * 128 + p.wn * 64 + c;
     float av[TM][4][8];
@@ -582,8 +583,8 @@ struct PlainOp {
   elt* out;  // [rows][w.n]
   __device__ __forceinline__ int stages() const { return x.k / 128; }
   typedef LoadRows LoadB;
-  __device__ __forceinline__ void init(int e, int m0, int m_end, int nt, Load& la,
-                                       LoadB& lb, Scales& sc, int tid) const {
+  __device__ __forceinline__ void init(int e, int m0, int m_end, int nt, Load& la, LoadB& lb,
+                                       Scales& sc, int tid) const {
     x.init(m0, m_end, la, sc, tid);
     w.init(e, nt, lb, sc, tid);
   }
@@ -625,8 +626,8 @@ struct DgradActOp {
   int F, ld2F;
   __device__ __forceinline__ int stages() const { return x.k / 128; }
   typedef LoadRows LoadB;
-  __device__ __forceinline__ void init(int e, int m0, int m_end, int nt, Load& la,
-                                       LoadB& lb, Scales& sc, int tid) const {
+  __device__ __forceinline__ void init(int e, int m0, int m_end, int nt, Load& la, LoadB& lb,
+                                       Scales& sc, int tid) const {
     x.init(m0, m_end, la, sc, tid);
     w.init(e, nt, lb, sc, tid);
   }

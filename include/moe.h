@@ -512,7 +512,7 @@ int moe_shared_expert_wgrad(const moe_shape* s, int64_t F_s, const void* x, cons
  * e4m3 values q (the OCP 8-bit float with four exponent and three mantissa
  * bits, largest value 448, no infinities) and one scale byte s per block of
  * MOE_FP8_BLOCK values along the product's reduction axis; it stands for
- *   q * 2^(s - 127).
+ *   q * 2^(s - 127),  0 <= s <= 254.
  * A scale is the smallest power of two with max|x| <= 448 * scale over the
  * block's finite values (s = 127 for a block of zeros, never below 0), and
  * q = x / scale rounded to nearest even; a value that is not finite becomes

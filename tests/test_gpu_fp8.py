@@ -321,6 +321,50 @@ def test_dgrad(name, dtype, gather):
     L.check_dgrad(L.dgrad())
 
 
+@pytest.mark.parametrize("T", [4, 8224])
+def test_weights_past_32_bits(T):
+    """256 experts of 4096 x 4096 (8.6 GB of gate and up): the rows of the last expert,
+    forward and gradient, for a few rows and for tiles."""
+    d = F = 4096
+    E, K = 256, 8
+    s = M.make_shape(T, d, F, E, 0, E, K, "bf16")
+    gen = torch.Generator(device="cuda").manual_seed(T)
+    g = lambda *sh, std=1.0: torch.empty(sh, dtype=torch.bfloat16,
+                                         device="cuda").normal_(0, std, generator=gen)
+    W = [g(E, 2 * F, d, std=d ** -0.5), g(E, d, F, std=F ** -0.5)]
+    w = M.Fp8Weights(s)
+    M.moe_quant_weights_fp8(s, W[0], W[1], w)
+    del W
+    ws = torch.empty(max(M.moe_fp8_workspace_bytes(s), M.moe_workspace_bytes(s)),
+                     dtype=torch.uint8, device="cuda")
+    idx = torch.stack([(torch.arange(T) * 37 + 249 + k * 31) % E for k in range(K)], 1)
+    idx[:4, 0] = 255
+    idx[:4, 1:] = torch.arange(1, K) * 5
+    i32 = lambda *sh: torch.zeros(*sh, dtype=torch.int32, device="cuda")
+    counts, offsets, tiles, rop, por = i32(E), i32(E + 1), i32(E + 1), i32(T * K), i32(T * K)
+    M.moe_dispatch(s, None, idx.to(torch.int32).cuda(), counts, offsets, rop, por, tiles, None, ws)
+    x, h = g(T, d), g(T * K, 2 * F)
+    q = torch.zeros(T, d, device="cuda").to(torch.float8_e4m3fn)
+    qs = torch.zeros(T, M.moe_fp8_scale_ld(d), dtype=torch.uint8, device="cuda")
+    M.moe_quant_rows_fp8(s, x, T, None, q, qs)
+    gates = torch.rand(T * K, device="cuda", generator=gen) + 0.05
+    out = {n: g(T * K, c) for n, c in (("h", 2 * F), ("y", d), ("dh", 2 * F), ("dx", d))}
+    M.moe_expert_ffn_fwd_fp8(s, q, qs, por, offsets, tiles, w, out["h"], None, out["y"], ws)
+    M.moe_ffn_dgrad_fp8(s, q, qs, por, gates, h, offsets, tiles, w, out["dh"], out["dx"], None, ws)
+    # the last expert's rows as a layer of one expert
+    lo, hi = int(offsets[E - 1]), int(offsets[E])
+    lo = max(lo, hi - 40)
+    assert hi - lo >= 4
+    L = object.__new__(Layer)
+    L.dtype, L.gather, L.d, L.F, L.K, L.E_l = "bf16", True, d, F, K, 1
+    L.N, L.off, L.pair = hi - lo, np.array([0, hi - lo]), host(por)[lo:hi]
+    L.q, L.qs, L.gates, L.h = q, qs, host(gates).astype(np.float32), h[lo:hi]
+    L.w = type("W", (), {n: getattr(w, n)[E - 1:] for n in ("gu", "gu_s", "down", "down_s")})
+    part = {n: t[lo:hi] for n, t in out.items()}
+    L.check_forward({"h": part["h"], "a": None, "y": part["y"]})
+    L.check_dgrad({"dh": part["dh"], "dx": part["dx"], "ag": None})
+
+
 @pytest.mark.parametrize("T,E", [(40, 8), (700, 4)])
 def test_no_local_rows(T, E):
     """Every token is routed outside the window: nothing is written."""
