@@ -454,20 +454,20 @@ def _chk_all(s, fn, tensors):
 
     if not _DTYPES:
         for dt in (MOE_F32, MOE_BF16, MOE_F16):
-            for kind in (_DATA, _F32, _I32, _FP8, _U8):
-                _DTYPES[kind, dt] = _torch_dtype(kind, MoeShape(dtype=dt))
-    dev, dt = None, s.dtype
+            _DTYPES[dt] = {kind: _torch_dtype(kind, MoeShape(dtype=dt))
+                           for kind in (_DATA, _F32, _I32, _FP8, _U8)}
+    want = _DTYPES.get(s.dtype) or {}
+    # no tensor is on a device before the first use of one (-1 is the host's)
+    dev = torch.cuda.current_device() if torch.cuda.is_initialized() else -2
     for name, t, kind, numel, optional in tensors:
         if t is None and optional:
             continue
-        if not (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype is _DTYPES.get((kind, dt))
-                and t.is_contiguous() and t.numel() >= numel):
+        if not (isinstance(t, torch.Tensor) and t.dtype is want.get(kind)
+                and t.get_device() == dev and t.is_contiguous() and t.numel() >= numel):
             _chk(s, fn, name, t, kind, numel, optional)
-        if dev is None:
-            dev = torch.cuda.current_device()
-        if t.get_device() != dev:
-            raise MoeError(MOE_ERR_ARG, f"{fn}: {name} is on {t.device}, the current device is "
-                                        f"cuda:{dev}")
+            if t.get_device() != dev:
+                raise MoeError(MOE_ERR_ARG, f"{fn}: {name} is on {t.device}, the current device "
+                                            f"is cuda:{dev}")
 
 
 def moe_fp8_scale_ld(k: int) -> int:
