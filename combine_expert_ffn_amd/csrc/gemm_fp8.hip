@@ -284,7 +284,7 @@ __device__ __forceinline__ void slice(const i32x8_t (&a)[TM], i32x8_t (&an)[TM],
 // The block of the reduction after k, around its end.
 __device__ __forceinline__ int after(int k, int nk) { return k + 1 < nk ? k + 1 : 0; }
 
-// The reduction over nk blocks from block k0 around; the first stage is in the first
+// The reduction over nk blocks from block k0 around (PlainOp::ROTATE); the first stage is in the first
 // buffer, the second is being copied to the other.  below: the tile has rows past
 // the first 128.  idle: the wave's 64 rows lie past the tile's last, so it only copies (2 %
 // of the time at 1024 rows per expert, whose last tiles are half empty).
@@ -517,6 +517,7 @@ struct GateUpOp {
   elt *h, *a;
   uint8_t *aq, *as;
   int F, ldF;
+  static constexpr bool ROTATE = false;
   __device__ __forceinline__ int stages() const { return x.k / 128; }
   typedef Load LoadB;
   __device__ __forceinline__ void init(int e, int m0, int m_end, int nt, Load& la, LoadB& lb,
@@ -581,6 +582,17 @@ struct GateUpOp {
 
 // Products whose result is stored as it is: forward GEMM2 (y_p = a^ . W_down^T) and
 // the second of the dgrad (dx_p = dh^ . W_gu, with the transposed weights).
+// ROTATE: the blocks of an XCD start at different blocks of the reduction.  Its CUs
+// work on consecutive tiles; in step, all that share a panel ask for its lines at once
+// and wait for memory together, started apart one fetches a line and the others find
+// it in L2.  bf16, 131072 rows, us in step and rotated, down and input gradient: 64 experts of
+// 2048 x 768 320 / 287 and 486 / 439, of 4096 x 1024 377 / 350 and 613 / 562, of 2048 x 1408
+// 462 / 426 and 780 / 740, of 1024 x 512 126 / 116 and 183 / 171, of 1024 x 1024 185 / 179 and
+// 297 / 288; fp16 within 3 % either way.  The products with SwiGLU epilogues gain nothing (gate
+// and up, activation gradient: 491 / 478 and 438 / 440, 614 / 610 and 458 / 463, 870 / 868 and
+// 814 / 831, 194 / 194 and 255 / 252, 395 / 396 and 469 / 463).  A row's float32 sum thus starts
+// where its CU does, and its last bits with it; a start by the column tile alone would not
+// depend on the row's place, and takes 312 and 478 us for 128 experts instead of 287 and 457.
 template <class E>
 struct PlainOp {
   typedef E type;
@@ -588,6 +600,7 @@ struct PlainOp {
   Rows x;
   Cols w;
   elt* out;  // [rows][w.n]
+  static constexpr bool ROTATE = true;
   __device__ __forceinline__ int stages() const { return x.k / 128; }
   typedef LoadRows LoadB;
   __device__ __forceinline__ void init(int e, int m0, int m_end, int nt, Load& la, LoadB& lb,
@@ -631,6 +644,7 @@ struct DgradActOp {
   elt *dh, *ag;
   uint8_t *dq, *ds;  // [rows][2F], [rows][ld2F]
   int F, ld2F;
+  static constexpr bool ROTATE = false;
   __device__ __forceinline__ int stages() const { return x.k / 128; }
   typedef LoadRows LoadB;
   __device__ __forceinline__ void init(int e, int m0, int m_end, int nt, Load& la, LoadB& lb,
@@ -701,18 +715,6 @@ struct DgradActOp {
   }
 };
 
-// The 32 CUs of an XCD work on consecutive tiles: n_tiles column tiles of each row
-// tile.  In step, all that share an operand panel ask for its lines at once and wait
-// for memory together; started at different blocks of the reduction, one fetches
-// a line and the others find it in L2.  That needs the panels of 32 tiles to stay there
-// (4 MB; 32 KB per panel and block): 128 experts of 2048 x 768, 131072 rows, down (2.3 MB) 335 ->
-// 288 us, input gradient (4.7 MB) 520 -> 461; gate and up (6 MB) 530 -> 532, activation
-// gradient (7 MB) 459 -> 471.
-__device__ __forceinline__ bool panels_fit(int n_tiles, int nk) {
-  const int cols = n_tiles < 32 ? n_tiles : 32;
-  return (cols + (31 + cols) / cols) * nk <= 160;
-}
-
 // Row-grouped product over the plan's tiles.  The next tile's first stage is copied
 // while a tile's epilogue runs, and ahead of its stores: a wave's memory operations
 // complete in order.
@@ -730,7 +732,6 @@ __global__ __launch_bounds__(NT) void fp8_kernel(Op op, const int32_t* __restric
   __syncthreads();
   Sched sch(s_to[E_l] * n_tiles);
   const int tid = threadIdx.x, nk = op.stages();
-  const bool rotate = panels_fit(n_tiles, nk);
   // LDS address of this wave's part of buffer 0
   const uint32_t lds = (uint32_t)__builtin_amdgcn_readfirstlane(
       (int)((uint32_t)(uintptr_t)(lds_u8_t*)smem + (threadIdx.x >> 6) * 1024u));
@@ -738,7 +739,7 @@ __global__ __launch_bounds__(NT) void fp8_kernel(Op op, const int32_t* __restric
   typename Op::LoadB lb;
   Scales sc;
   int nt, e, m0, m_end, half;
-  const int k0 = rotate ? (int)(blockIdx.x / 8) % nk : 0;
+  const int k0 = Op::ROTATE ? (int)(blockIdx.x / 8) % nk : 0;
   // Finds the next unit with rows and starts its copies; false behind the last.
   auto locate = [&]() {
     for (; sch.u < sch.units; sch.u += sch.step) {  // block-uniform

@@ -531,8 +531,10 @@ int moe_shared_expert_wgrad(const moe_shape* s, int64_t F_s, const void* x, cons
  * reduction) at 2^-13 of the largest of the 8.  On normally distributed operands
  * that is 1.5e-5 of a sum, rms, where rounding the sum to bf16 is 1.7e-3; a sum
  * whose large products cancel may lose its small ones.
- *   q buffers and workspaces are 16-byte aligned, scale buffers 4-byte
- * (MOE_ERR_ARG).
+ *   Equal calls give equal bits.  h, a, dh and ag of a row depend on its own
+ * operands and the shape alone.  So do yp and dxp with few rows per expert; with
+ * more, the float32 sum of a row may start at another block of the reduction
+ * beside other rows, and its last bits differ by that order.
  */
 #define MOE_FP8_BLOCK 128
 
