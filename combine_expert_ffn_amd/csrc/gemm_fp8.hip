@@ -39,6 +39,8 @@
 // slices, four waves that copy while the other four store.
 #include "moe_fp8.h"
 
+#include <algorithm>
+
 namespace moe {
 namespace {
 
@@ -849,11 +851,12 @@ int ffn_dgrad_t(const moe_shape* s, const void* dq, const uint8_t* ds, const int
 }  // namespace
 
 size_t fp8_workspace_bytes(const moe_shape* s) {
-  // the gradient's share is the larger, and holds the forward's either way
-  if (fp8_small(s, true)) return align_up(fp8_small_workspace_bytes(s) + 256, 256);
+  // the gradient's share is the larger, and holds the forward's either way; the
+  // larger of both kernels', so that it never falls as T grows
   const size_t rows = (size_t)(s->T * s->K);
   const size_t b = align_up(rows * 2 * s->F, 256) + align_up(rows * fp8_scale_ld(2 * s->F), 256);
-  return b < 256 ? 256 : b;
+  const size_t few = align_up(fp8_small_workspace_bytes(s), 256);
+  return std::max({b, few, (size_t)256});
 }
 
 int launch_ffn_fwd_fp8(const moe_shape* s, const void* xq, const uint8_t* xs,

@@ -17,6 +17,8 @@
 
 #include <math.h>
 
+#include <algorithm>
+
 namespace moe {
 namespace {
 
@@ -440,13 +442,17 @@ int ffn_dgrad_t(const moe_shape* s, const void* dq, const uint8_t* ds, const int
 // 47 / 44 and 55 / 67, at 64 59 / 44 and 69 / 68; 8 of 2048 x 768 at 64 36 / 38 and 39 / 56, at
 // 128 50 / 40 and 59 / 58; 4 of 640 x 384 at 256 24 / 32 and 28 / 49.  fp16: 8 of 2048 x 1408 at
 // 64 59 / 59 and 69 / 86, at 128 104 / 60 and 121 / 89.
-bool fp8_small(const moe_shape* s, bool dgrad) {
-  const int64_t mean = cdiv(s->T * s->K, s->E);
+static int64_t most_mean(const moe_shape* s, bool dgrad) {
   const int64_t most = (s->dtype == MOE_BF16 ? 800000000 : 1400000000) + (dgrad ? 500000000 : 0);
-  return mean <= 256 && s->E_l * s->F * s->d * (mean - 11) <= most;
+  return std::min<int64_t>(256, 11 + most / (s->E_l * s->F * s->d));
 }
+bool fp8_small(const moe_shape* s, bool dgrad) {
+  return cdiv(s->T * s->K, s->E) <= most_mean(s, dgrad);
+}
+// For the longest batch of at most T tokens that these kernels take.
 size_t fp8_small_workspace_bytes(const moe_shape* s) {
-  return (size_t)(s->T * s->K * 2 * s->F) * sizeof(float);
+  const int64_t rows = std::min(s->T * s->K, s->E * most_mean(s, true));
+  return (size_t)(rows * 2 * s->F) * sizeof(float);
 }
 
 int launch_ffn_fwd_fp8_small(const moe_shape* s, const void* xq, const uint8_t* xs,

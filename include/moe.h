@@ -575,7 +575,9 @@ int moe_quant_rows_fp8(const moe_shape* s, const void* src, int64_t rows, const 
 int moe_quant_weights_fp8(const moe_shape* s, const void* W_gu, const void* W_down,
                           const moe_fp8_weights* w, hipStream_t stream);
 
-/* Bytes of workspace moe_expert_ffn_fwd_fp8 and moe_ffn_dgrad_fp8 need. */
+/* Bytes of workspace moe_expert_ffn_fwd_fp8 and moe_ffn_dgrad_fp8 need.  They never
+ * fall as T grows (the rest of the shape unchanged): the workspace of the longest
+ * batch does for every shorter one. */
 size_t moe_fp8_workspace_bytes(const moe_shape* s);
 
 /*
