@@ -345,22 +345,26 @@ __global__ __launch_bounds__(64 * WAVES) void small_second_kernel(
 // where that and 16 rows per block leave one block per CU or more (every block reads, and
 // for the second product quantises, all of its rows: at 128 rows, 2 experts of 2048 x 2048,
 // 29 us against 71 for the activation gradient's second product).  G: as many token groups
-// per pass as the rows fill, fewer where blocks are few, down to one; the passes are
-// spread over the grid's z until there are four blocks per CU.
+// per pass as the rows fill, fewer where blocks are few, down to one.  An expert may hold
+// every token: all passes that this takes are spread over the grid's z, as far as four
+// blocks per CU (surplus blocks leave at once: nothing measurable on even loads).  8 of
+// 64 experts of 2048 x 768, 256 tokens, K = 1, z for the rows of an even load and for every
+// token: even 21 and 20 us, Zipf 1.1 74 and 49, all on one expert 126 and 76.
 struct Shape {
   int G, S;
+  int64_t passes;  // of a block whose expert holds every token
   dim3 grid;
   Shape(const moe_shape* s, int cols, bool may_widen) {
     const int64_t pairs = s->T * s->K;
     const double mean = (double)pairs / (double)s->E;
     const int64_t rows = (int64_t)(mean + 2 * sqrt(mean)) + 1;
-    const int64_t slots = pairs < s->E_l ? pairs : s->E_l;
+    const int64_t slots = std::max<int64_t>(1, std::min(pairs, s->E_l));
     S = may_widen && slots * cols / 64 * cdiv(rows, 16) >= 256 ? 4 : 1;
     const int64_t blocks = slots * cols / (16 * S);
     G = rows <= 16 ? 1 : (rows <= 32 ? 2 : 4);
     while (G > 1 && blocks * cdiv(rows, 16 * G) < (S == 1 ? 512 : 256)) G /= 2;
-    int64_t z = cdiv(rows, 16 * G);
-    if (z > cdiv(1024, blocks)) z = cdiv(1024, blocks);
+    const int64_t z = std::max<int64_t>(1, std::min(cdiv(s->T, 16 * G), cdiv(1024, blocks)));
+    passes = cdiv(s->T, 16 * G * z);
     grid = dim3((unsigned)(cols / (16 * S)), (unsigned)slots, (unsigned)z);
   }
 };
@@ -442,12 +446,20 @@ int ffn_dgrad_t(const moe_shape* s, const void* dq, const uint8_t* ds, const int
 // 47 / 44 and 55 / 67, at 64 59 / 44 and 69 / 68; 8 of 2048 x 768 at 64 36 / 38 and 39 / 56, at
 // 128 50 / 40 and 59 / 58; 4 of 640 x 384 at 256 24 / 32 and 28 / 49.  fp16: 8 of 2048 x 1408 at
 // 64 59 / 59 and 69 / 86, at 128 104 / 60 and 121 / 89.
+// These are even loads, and the time here follows the fullest expert, whose passes a block
+// makes one after another.  So no block may need more than 8 with every token on one expert:
+// over the 362 calls tried that this and the limits above let through (four shapes from
+// 640 x 384 to 4096 x 1024, 4 to 128 experts, K = 1 to 8, 16 to 2048 tokens), small over tiles is
+// 0.62 on even loads, 0.84 with Zipf 1.1 and 0.98 with all tokens on the same K experts
+// (geometric means; worst 7.8), without it 0.65, 1.13 and 1.45 (worst 20.5, and 26 at 16384
+// tokens, 64 experts of 512 x 384, all on one: 859 / 33).
 static int64_t most_mean(const moe_shape* s, bool dgrad) {
   const int64_t most = (s->dtype == MOE_BF16 ? 800000000 : 1400000000) + (dgrad ? 500000000 : 0);
   return std::min<int64_t>(256, 11 + most / (s->E_l * s->F * s->d));
 }
 bool fp8_small(const moe_shape* s, bool dgrad) {
-  return cdiv(s->T * s->K, s->E) <= most_mean(s, dgrad);
+  return cdiv(s->T * s->K, s->E) <= most_mean(s, dgrad) &&
+         std::max(Shape(s, (int)s->F, dgrad).passes, Shape(s, (int)s->d, true).passes) <= 8;
 }
 // For the longest batch of at most T tokens that these kernels take.
 size_t fp8_small_workspace_bytes(const moe_shape* s) {
