@@ -470,6 +470,25 @@ def _chk_all(s, fn, tensors):
                                             f"is cuda:{dev}")
 
 
+class _Bound:
+    """Tensors whose addresses a C struct holds between calls.  They are compared on
+    every call (0.08 us each), and bound and checked again where one has moved
+    (``.data =``, ``set_``, ``resize_``).  A detached alias of each keeps its
+    allocation, so that an address cannot come to mean another one."""
+
+    def _hold(self, tensors):
+        self._held = list(tensors)
+        self._kept = [t.detach() for t in self._held]
+        self._ptrs = [t.data_ptr() for t in self._held]
+
+    def _current(self):
+        import torch
+
+        if self._ptrs is None or list(map(torch.Tensor.data_ptr, self._held)) != self._ptrs:
+            self._ptrs = None               # stays so if a check below raises
+            self._bind()
+
+
 def moe_fp8_scale_ld(k: int) -> int:
     """Bytes per row of scales of a matrix with k values per row."""
     return lib().moe_fp8_scale_ld(int(k))
@@ -479,42 +498,59 @@ def moe_fp8_workspace_bytes(s: MoeShape) -> int:
     return lib().moe_fp8_workspace_bytes(C.byref(s))
 
 
-class Fp8Weights:
+class Fp8Weights(_Bound):
     """The routed experts' weights in 8 bits for shape ``s`` (moe_fp8_weights in
     include/moe.h): e4m3 tensors gu, down (and transposed guT, downT) with their
     uint8 scales, allocated here, or given (gu, gu_s, down and down_s, and all four
     transposed ones or none).  With ``transposed=False`` the transposed copies,
-    which only the dgrad reads, are not allocated."""
+    which only the dgrad reads, are not allocated.  The tensors are attributes; one
+    that is replaced, or whose memory is, is checked and used from the next call on."""
 
     def __init__(self, s: MoeShape, device="cuda", transposed=True, **tensors):
         import torch
 
-        d, F, E_l = s.d, s.F, s.E_l
         if tensors:
             given = set(tensors)
             transposed = given == set(FP8_WEIGHT_FIELDS)
             if not transposed and given != {"gu", "gu_s", "down", "down_s"}:
                 raise ValueError(f"Fp8Weights: given {sorted(given)}, not gu, gu_s, down, down_s "
                                  "(and the four transposed tensors)")
-        b = MOE_FP8_BLOCK
+        self.shape = (s.d, s.F, s.E_l)
+        for name, (shape, kind) in self._fields().items():
+            t = tensors.get(name)
+            if t is None and (transposed or "T" not in name):
+                t = torch.empty(shape, dtype=_torch_dtype(kind, s), device=device)
+            setattr(self, name, t)
+        self._bind()
+
+    def __setattr__(self, name, value):
+        object.__setattr__(self, name, value)
+        if name in FP8_WEIGHT_FIELDS:
+            self._ptrs = None
+
+    def _fields(self):
+        """{name: (shape, kind)}"""
+        d, F, E_l = self.shape
+        b, out = MOE_FP8_BLOCK, {}
         for n, rows, k in (("gu", 2 * F, d), ("down", d, F), ("guT", d, 2 * F), ("downT", F, d)):
-            ld = (k // b + 3) // 4 * 4
-            for name, shape, kind in ((n, (E_l, rows, k), _FP8),
-                                      (n + "_s", (E_l, rows // b, ld), _U8)):
-                t = tensors.get(name)
-                if t is None and (transposed or not n.endswith("T")):
-                    t = torch.empty(shape, dtype=_torch_dtype(kind, s), device=device)
-                _chk(s, "Fp8Weights", name, t, kind, shape[0] * shape[1] * shape[2],
-                     optional=n.endswith("T"))
-                if t is not None and name != "gu" and t.device != self.gu.device:
-                    raise MoeError(MOE_ERR_ARG, f"Fp8Weights: {name} is on {t.device}, gu on "
-                                                f"{self.gu.device}")
-                setattr(self, name, t)
-        self.shape = (d, F, E_l)
+            out[n] = (E_l, rows, k), _FP8
+            out[n + "_s"] = (E_l, rows // b, (k // b + 3) // 4 * 4), _U8
+        return out
+
+    def _bind(self):
+        for name, (shape, kind) in self._fields().items():
+            t = getattr(self, name)
+            _chk(MoeShape(), "Fp8Weights", name, t, kind, shape[0] * shape[1] * shape[2],
+                 optional="T" in name)
+            if t is not None and t.device != self.gu.device:
+                raise MoeError(MOE_ERR_ARG, f"Fp8Weights: {name} is on {t.device}, gu on "
+                                            f"{self.gu.device}")
         self.device = self.gu.get_device()
         self.struct = MoeFp8Weights(*[_p(getattr(self, n)) for n in FP8_WEIGHT_FIELDS])
+        self._hold(t for n in FP8_WEIGHT_FIELDS if (t := getattr(self, n)) is not None)
 
     def check(self, fn, s: MoeShape):
+        self._current()
         if self.shape != (s.d, s.F, s.E_l):
             raise MoeError(MOE_ERR_ARG, f"{fn}: weights are for (d, F, E_l) = {self.shape}, the "
                                         f"shape has {(s.d, s.F, s.E_l)}")
@@ -586,19 +622,22 @@ def moe_ffn_dgrad_fp8(s, dq, ds, pair_of_row, gates, h, offsets, tile_offsets, w
 
 
 # ---- weight update ----------------------------------------------------------
-class AdamWTensors:
-    """The tensors of an AdamW step, checked once and kept for many steps.  Each
-    is a dict: param (float32, bfloat16 or float16), grad (float32), m and v
+class AdamWTensors(_Bound):
+    """The tensors of an AdamW step, checked and kept for many steps (and checked
+    again where the memory of one has moved).  Each is a dict: param (float32, bfloat16 or float16), grad (float32), m and v
     (float32, or float8_e4m3fn with uint8 scales m_s and v_s of
     ceil(n / 128) elements), and optionally master (float32) and weight_decay.
     What the step writes must not overlap anything else in the list."""
 
     def __init__(self, tensors):
+        self.tensors = [dict(t) for t in tensors]
+        self._bind()
+
+    def _bind(self):
         import torch
 
         fn = "AdamWTensors"
         dts = {torch.float32: MOE_F32, torch.bfloat16: MOE_BF16, torch.float16: MOE_F16}
-        self.tensors = [dict(t) for t in tensors]
         self.device = None
         self.array = (MoeAdamwTensor * max(1, len(self.tensors)))()
         for i, t in enumerate(self.tensors):
@@ -635,6 +674,8 @@ class AdamWTensors:
                 if (written or w) and lo < e:
                     raise MoeError(MOE_ERR_ARG, f"{fn}: {name} and {other} share memory")
             end[written] = max(end[written], (hi, name))
+        self._hold(x for t in self.tensors for name in ("param", "master", "grad", "m", "v", "m_s",
+                                                        "v_s") if (x := t.get(name)) is not None)
 
 
 def moe_adamw(tensors, lr, beta1=0.9, beta2=0.999, eps=1e-8, step=1, grad_scale=1.0,
@@ -642,6 +683,8 @@ def moe_adamw(tensors, lr, beta1=0.9, beta2=0.999, eps=1e-8, step=1, grad_scale=
     """tensors: an AdamWTensors (or the list of dicts to make one of)."""
     if not isinstance(tensors, AdamWTensors):
         tensors = AdamWTensors(tensors)
+    else:
+        tensors._current()
     if grad_scale_dev is not None:
         _chk_all(MoeShape(dtype=MOE_F32), "moe_adamw",
                  (("grad_scale_dev", grad_scale_dev, _F32, 1, False),))
