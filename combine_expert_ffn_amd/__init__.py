@@ -468,6 +468,7 @@ def _chk_all(s, fn, tensors):
             if t.get_device() != dev:
                 raise MoeError(MOE_ERR_ARG, f"{fn}: {name} is on {t.device}, the current device "
                                             f"is cuda:{dev}")
+    return dev
 
 
 class _Bound:
@@ -584,12 +585,15 @@ def moe_quant_weights_fp8(s, W_gu, W_down, w: Fp8Weights, stream=None):
 def _chk_fp8(s, fn, q, qs, pair_of_row, offsets, tile_offsets, ws, more):
     cap, d = s.T * s.K, s.d
     rows = cap if pair_of_row is None else s.T
-    _chk_all(s, fn, (("quantised rows", q, _FP8, rows * d, False),
-                     ("row scales", qs, _U8, rows * ((d // MOE_FP8_BLOCK + 3) // 4 * 4), False),
-                     ("pair_of_row", pair_of_row, _I32, cap, True),
-                     ("offsets", offsets, _I32, s.E_l + 1, False),
-                     ("tile_offsets", tile_offsets, _I32, s.E_l + 1, False)) + more)
+    dev = _chk_all(s, fn, (("quantised rows", q, _FP8, rows * d, False),
+                           ("row scales", qs, _U8, rows * ((d // MOE_FP8_BLOCK + 3) // 4 * 4),
+                            False),
+                           ("pair_of_row", pair_of_row, _I32, cap, True),
+                           ("offsets", offsets, _I32, s.E_l + 1, False),
+                           ("tile_offsets", tile_offsets, _I32, s.E_l + 1, False)) + more)
     _chk_ws(fn, ws)
+    if ws is not None and ws.get_device() != dev:
+        raise MoeError(MOE_ERR_ARG, f"{fn}: ws is on {ws.device}, the current device is cuda:{dev}")
 
 
 def moe_expert_ffn_fwd_fp8(s, xq, xs, pair_of_row, offsets, tile_offsets, w: Fp8Weights, h, a, yp,
@@ -624,10 +628,11 @@ def moe_ffn_dgrad_fp8(s, dq, ds, pair_of_row, gates, h, offsets, tile_offsets, w
 # ---- weight update ----------------------------------------------------------
 class AdamWTensors(_Bound):
     """The tensors of an AdamW step, checked and kept for many steps (and checked
-    again where the memory of one has moved).  Each is a dict: param (float32, bfloat16 or float16), grad (float32), m and v
-    (float32, or float8_e4m3fn with uint8 scales m_s and v_s of
-    ceil(n / 128) elements), and optionally master (float32) and weight_decay.
-    What the step writes must not overlap anything else in the list."""
+    again where the memory of one has moved).  Each is a dict: param (float32,
+    bfloat16 or float16), grad (float32), m and v (float32, or float8_e4m3fn with
+    uint8 scales m_s and v_s of ceil(n / 128) elements), and optionally master
+    (float32) and weight_decay.  What the step writes must not overlap anything
+    else in the list."""
 
     def __init__(self, tensors):
         self.tensors = [dict(t) for t in tensors]

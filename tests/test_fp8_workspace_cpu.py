@@ -1,6 +1,8 @@
-"""A workspace sized for the longest batch does for every shorter one."""
+"""The 8-bit calls' workspace: sized for the longest batch it does for every shorter
+one, and it is on the device of the call."""
 
 import pytest
+import torch
 
 import combine_expert_ffn_amd as M
 
@@ -26,3 +28,17 @@ def test_workspace_never_falls_as_the_batch_grows(name, dtype):
         # a quantised row and its scales, or a few float32 rows: no more than the larger
         assert 256 <= need <= max(256, T * K * 8 * F + 512), T
         last = need
+
+
+def test_workspace_on_another_device_is_refused(monkeypatch):
+    monkeypatch.setattr(M, "_chk_all", lambda *a: 0)     # all tensors are on device 0
+    monkeypatch.setattr(M, "_chk_ws", lambda *a: None)
+    s = M.make_shape(4, 256, 128, 2, 0, 2, 1, "bf16")
+    ws = torch.zeros(1 << 16, dtype=torch.uint8)         # on the host, device -1
+    reached = pytest.raises(AttributeError)              # the weights, None here, come after
+    for on, outcome in ((-1, pytest.raises(M.MoeError)), (0, reached)):
+        monkeypatch.setattr(torch.Tensor, "get_device", lambda t: on)
+        with outcome:
+            M.moe_expert_ffn_fwd_fp8(s, ws, ws, None, ws, ws, None, None, None, ws, ws, 0)
+        with pytest.raises(M.MoeError) if on else pytest.raises(AttributeError):
+            M.moe_ffn_dgrad_fp8(s, ws, ws, None, None, ws, ws, ws, None, ws, ws, None, ws, 0)
