@@ -91,7 +91,7 @@ __device__ __forceinline__ void copy_rows(uint32_t off, u32x4_t r, uint32_t at, 
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
                :
                : "s"(lds), "v"(off), "s"(r), "s"(at)
-               : "memory");
+               : "memory", "m0");
 }
 
 // One operand's 256 rows: 4 copies per wave and stage, 64 rows apart.
