@@ -135,9 +135,10 @@ def random_bits(n, index, seed, step):
             (_mul(x, 0x9E3779B1) >> np.uint64(12)).astype(np.int64))
 
 
-def quant_random(x, rnd):
+def quant_random(x, rnd, least=False):
     """[n] -> (values, bytes): blocks of 128, rounded up with probability rnd /
-    2^20's share of the step: floor(|y| / step + rnd 2^-20) steps."""
+    2^20's share of the step: floor(|y| / step + rnd 2^-20) steps.  least: what is
+    not zero is at least one step, as the second moment's root is stored."""
     n = x.size
     pad = np.concatenate([x, np.zeros(-n % BLOCK)]).reshape(-1, BLOCK)
     byte = scale_byte(_amax(pad, 1))
@@ -145,7 +146,10 @@ def quant_random(x, rnd):
         y = (pad * np.ldexp(1.0, 127 - byte)[:, None]).reshape(-1)[:n]
         _, ex = np.frexp(np.where(np.isfinite(y), y, 0.0))
         step = np.ldexp(1.0, np.maximum(ex - 1, -6) - 3)
-        q = np.copysign(np.floor(np.abs(y) / step + rnd * 2.0 ** -20) * step, y)
+        q = np.floor(np.abs(y) / step + rnd * 2.0 ** -20) * step
+        if least:
+            q = np.where(np.abs(y) > 0, np.maximum(q, 2.0 ** -9), q)
+        q = np.copysign(q, y)
     return np.where(np.isfinite(y), q, np.nan), byte
 
 
