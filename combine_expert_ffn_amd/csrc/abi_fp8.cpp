@@ -27,8 +27,7 @@ static int validate_fp8_shape(const moe_shape* s, const char* fn) {
   return MOE_OK;
 }
 
-// The checks the two product calls share.  rows_in: rows of the quantised
-// operand that the GEMM addresses from one base (0 where it is rebased).
+// The checks the two product calls share.
 static int validate_fp8_product(const moe_shape* s, const char* fn, const void* q, const void* qs,
                                 const int32_t* pair_of_row, const void* ws, size_t ws_bytes) {
   if (!is16(s))

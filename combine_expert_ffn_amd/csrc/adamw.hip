@@ -39,17 +39,8 @@ struct Args {
   const float* scale_dev;
 };
 
-__device__ __forceinline__ float row16_max(float v) {
-  auto step = [](float x, int moved) { return fmaxf(x, __int_as_float(moved)); };
-  v = step(v, __builtin_amdgcn_update_dpp(0, __float_as_int(v), 0xB1, 0xF, 0xF, true));
-  v = step(v, __builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x4E, 0xF, 0xF, true));
-  v = step(v, __builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x141, 0xF, 0xF, true));
-  v = step(v, __builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x140, 0xF, 0xF, true));
-  return v;
-}
-
 // 32 well mixed bits of an element's number (xor-shift and multiply by odd
-// constants, twice); the top 20 of them, and the top 20 of one more product,
+// constants, twice; the constants are primes of a published 32-bit hash); the top 20 of them, and the top 20 of one more product,
 // are the two roundings' random numbers.
 __device__ __forceinline__ uint32_t mix(uint32_t x) {
   x ^= x >> 16;
@@ -127,7 +118,7 @@ __device__ __forceinline__ void store_q(uint8_t* q, uint8_t* s, int64_t blk, int
   float mx = 0.f;
 #pragma unroll
   for (int i = 0; i < 8; ++i) mx = fmaxf(mx, finite_abs(f[i]));
-  const int byte = fp8_scale_byte(row16_max(mx));
+  const int byte = fp8_scale_byte(lanes_max<16>(mx));
   const float inv = fp8_inv_scale(byte);
   uint32_t w[2] = {0, 0};
 #pragma unroll

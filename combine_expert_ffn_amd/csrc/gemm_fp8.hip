@@ -49,7 +49,6 @@ typedef int i32x8_t __attribute__((ext_vector_type(8)));
 typedef unsigned int u32x2_t __attribute__((ext_vector_type(2)));
 typedef unsigned int u32x4_t __attribute__((ext_vector_type(4)));
 typedef float f32x16_t __attribute__((ext_vector_type(16)));
-typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
 typedef __attribute__((address_space(3))) uint8_t lds_u8_t;
 
 struct BF16 {
@@ -218,15 +217,6 @@ struct Pos {
     return {l, w, w / WGN, w % WGN};
   }
 };
-
-// Eight e4m3 values (two registers) times a power of two, exact in bf16.
-__device__ __forceinline__ bf16x8_t widen(int lo, int hi, float scale) {
-  const bf16x2_t a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, scale, false);
-  const bf16x2_t b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, scale, true);
-  const bf16x2_t c = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, scale, false);
-  const bf16x2_t d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, scale, true);
-  return bf16x8_t{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
-}
 
 // One 64-deep slice: the MFMAs of the wave on a and b, and beside them the reads
 // of the next slice's fragments (an into its own registers, b's four one by one
@@ -494,18 +484,6 @@ __device__ __forceinline__ uint2 quant8(const float* f, float inv) {
   return uint2{pack_fp8(f[0] * inv, f[1] * inv, f[2] * inv, f[3] * inv),
                pack_fp8(f[4] * inv, f[5] * inv, f[6] * inv, f[7] * inv)};
 }
-// Largest value over rows of 8 or 16 lanes.
-template <int N>
-__device__ __forceinline__ float lanes_max(float v) {
-  auto step = [](float x, int moved) { return fmaxf(x, __int_as_float(moved)); };
-  v = step(v, __builtin_amdgcn_update_dpp(0, __float_as_int(v), 0xB1, 0xF, 0xF, true));
-  v = step(v, __builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x4E, 0xF, 0xF, true));
-  v = step(v, __builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x141, 0xF, 0xF, true));
-  if constexpr (N == 16)
-    v = step(v, __builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x140, 0xF, 0xF, true));
-  return v;
-}
-
 // forward GEMM1: [g, u] = x^ . W_gu^[e]^T, a = silu(g) u, quantised for GEMM2.
 // A tile is 128 outputs: the 128 tile columns of wave column wn are 64 gate
 // rows and the 64 up rows of the same outputs.  The tile's outputs are one

@@ -24,7 +24,6 @@ namespace {
 
 typedef int i32x4_t __attribute__((ext_vector_type(4)));
 typedef float f32x4_t __attribute__((ext_vector_type(4)));
-typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
 
 constexpr int WAVES = 4;
 // Blocks of 128 in flight per wave, for `sets` of 16 weight rows each.
@@ -62,14 +61,6 @@ __device__ __forceinline__ bool nth_expert(const int32_t* offsets, int E_l, int 
   return found;
 }
 
-// Eight e4m3 values (two registers) times a power of two, exact in bf16.
-__device__ __forceinline__ bf16x8_t widen(int lo, int hi, float scale) {
-  const bf16x2_t a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, scale, false);
-  const bf16x2_t b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, scale, true);
-  const bf16x2_t c = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, scale, false);
-  const bf16x2_t d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, scale, true);
-  return bf16x8_t{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
-}
 // A lane's 32 values of a block of 128: row lane % 16, values 32 (lane / 16) ..+31,
 // the same for both operands (the order within a block does not change its sum).
 struct Raw {

@@ -5,6 +5,8 @@
 
 namespace moe {
 
+typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
+
 int validate_shape(const moe_shape* s);  // abi.cpp
 
 // Bytes per row of scales for k values: a multiple of 4, so that four blocks'
@@ -46,6 +48,28 @@ __device__ __forceinline__ uint32_t pack_fp8(float a, float b, float c, float d)
 }
 __device__ __forceinline__ float finite_or_nan(float x) {
   return fabsf(x) < __builtin_inff() ? x : __builtin_nanf("");
+}
+
+// Largest value over each row of 8 or 16 lanes, in every lane of it: lanes swapped
+// within pairs and quads, then the halves of 8 and of 16 mirrored.
+template <int N>
+__device__ __forceinline__ float lanes_max(float v) {
+  auto step = [](float x, int moved) { return fmaxf(x, __int_as_float(moved)); };
+  v = step(v, __builtin_amdgcn_update_dpp(0, __float_as_int(v), 0xB1, 0xF, 0xF, true));
+  v = step(v, __builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x4E, 0xF, 0xF, true));
+  v = step(v, __builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x141, 0xF, 0xF, true));
+  if constexpr (N == 16)
+    v = step(v, __builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x140, 0xF, 0xF, true));
+  return v;
+}
+// Eight e4m3 values (two registers) times a power of two, exact in bf16
+// (from its smallest normal value on).
+__device__ __forceinline__ bf16x8_t widen(int lo, int hi, float scale) {
+  const bf16x2_t a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, scale, false);
+  const bf16x2_t b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, scale, true);
+  const bf16x2_t c = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, scale, false);
+  const bf16x2_t d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, scale, true);
+  return bf16x8_t{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
 }
 
 // ---------------------------------------------------------------------------

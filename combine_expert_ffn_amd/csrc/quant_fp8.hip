@@ -9,17 +9,6 @@
 namespace moe {
 namespace {
 
-// Largest value over each row of 16 lanes, in every lane of it: lanes swapped
-// within pairs and quads, then the halves of 8 and of 16 mirrored.
-__device__ __forceinline__ float row16_max(float v) {
-  auto step = [](float x, int moved) { return fmaxf(x, __int_as_float(moved)); };
-  v = step(v, __builtin_amdgcn_update_dpp(0, __float_as_int(v), 0xB1, 0xF, 0xF, true));
-  v = step(v, __builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x4E, 0xF, 0xF, true));
-  v = step(v, __builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x141, 0xF, 0xF, true));
-  v = step(v, __builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x140, 0xF, 0xF, true));
-  return v;
-}
-
 // Eight consecutive elements as floats.
 template <typename T>
 __device__ __forceinline__ void load8(const T* p, float* f) {
@@ -55,7 +44,7 @@ __global__ __launch_bounds__(256) void quant_rows_kernel(const T* __restrict__ s
   for (int64_t b = (int64_t)blockIdx.x * 16 + grp; b < blocks; b += (int64_t)gridDim.x * 16) {
     float f[8];
     load8(src + b * 128 + l * 8, f);
-    const int byte = fp8_scale_byte(row16_max(amax8(f)));
+    const int byte = fp8_scale_byte(lanes_max<16>(amax8(f)));
     *(uint2*)(q + b * 128 + l * 8) = quant8(f, fp8_inv_scale(byte));
     const int64_t row = b / kb;
     const int k = (int)(b - row * kb);
@@ -110,7 +99,7 @@ __global__ __launch_bounds__(256) void quant_weights_kernel(WMat m0, WMat m1, in
   for (int i = 0; i < 8; ++i) load8(src + (size_t)i * K, f[i]);
 #pragma unroll
   for (int i = 0; i < 8; ++i) mx = fmaxf(mx, amax8(f[i]));
-  mx = row16_max(mx);
+  mx = lanes_max<16>(mx);
   mx = fmaxf(mx, __shfl_xor(mx, 16, 64));
   mx = fmaxf(mx, __shfl_xor(mx, 32, 64));
   if ((tid & 63) == 0) wave_max[tid >> 6] = mx;
