@@ -30,11 +30,13 @@
 //    L2 (non-temporal), where they would push out the operands that 32 CUs share;
 //  * persistent grid over the dispatch plan's row tiles, one range per XCD.
 // What bounds it: moving operands to LDS and results out.  128 experts of 2048 x 768,
-// 131072 rows, bf16: gate and up 508 us (1.62 PFLOP/s), down 284 (1.45), activation gradient
-// 452 (which also reads h) and 459 (1.80).  With parts left out, gate and up / down:
-// fragment reads and MFMAs alone 300 / 168 us, copies alone 319 / 160 (184 / 106 where L2
-// has all), everything but the stores 452 / 225.  A wave's memory operations complete in
-// order, so a tile's stores (at the write rate of HBM) add up with the next one's copies.
+// 131072 rows, bf16, by the library's kernel timer: gate and up 509 us (1.62 PFLOP/s), down 289
+// (1.43), activation gradient 450 (which also reads h) and input gradient 457 (1.80); the matrix
+// cores are busy 43, 37, 24 and 47 % of that, and memory reads are 2.5, 1.1, 1.7 and 2.1 times
+// the operands.  In variants with parts left out, gate and up / down: fragment reads and MFMAs
+// alone 300 / 168 us, copies alone 319 / 160 (184 / 106 where L2 has all), everything but
+// the stores 452 / 225.  A wave's memory operations complete in order, so a tile's stores (at
+// the write rate of HBM) add up with the next one's copies.
 // Slower: two blocks of half the size per CU, four waves of 128 x 128, rings of 64-byte
 // slices, four waves that copy while the other four store.
 #include "moe_fp8.h"

@@ -1,8 +1,12 @@
 // The 8-bit expert products for few rows per expert (decoding, short prompts):
 // each is one pass over the active experts' weights, so what bounds them is how
 // fast those stream from memory.  A block takes 16 S weight rows (of both halves for
-// gate and up) of one expert; its four waves share the reduction by blocks of 128
-// and keep all of their weight bytes in flight, straight to registers.  The weight
+// gate and up) of one expert; its four waves share the reduction by blocks of 128,
+// whose weights go straight to registers.  As compiled, a wave asks for one block's
+// weights and rows at a time, behind the MFMAs of the one before (the loads that stand
+// ahead of them in reduce_blocks are moved past the loop's exit), and the second product for its
+// weights behind the quantisation: up to four memory latencies in a row, which other
+// waves cover where there are many and nothing does for a single token.  The weight
 // rows are the M side of 16 x 16 x 32 bf16 MFMAs, up to 16 G token rows the N side:
 // e4m3 values and their power-of-two scales are exact in bf16, so the products are
 // exact and only their float32 sums round, and the conversions (one instruction per
@@ -11,8 +15,8 @@
 // as it reads them (each wave its own blocks of 128, in registers), so no block
 // needs another's column maximum.
 // bf16 on an MI355X, forward: one token, 8 of 128 experts of 2048 x 768, 13.9 us (38 MB of
-// weights; two launches and their chains of latencies); 8 rows for each of the 128, 129 us
-// (604 MB, 4.7 TB/s, near the 5.0 of a large copy).
+// weights; two launches and their chains of latencies); 64 tokens, up to 9 rows for each of
+// the 128, 131 us (604 MB, 4.6 TB/s, near the 5.0 of a large copy).
 #include "moe_fp8.h"
 
 #include <math.h>
@@ -26,7 +30,7 @@ typedef int i32x4_t __attribute__((ext_vector_type(4)));
 typedef float f32x4_t __attribute__((ext_vector_type(4)));
 
 constexpr int WAVES = 4;
-// Blocks of 128 in flight per wave, for `sets` of 16 weight rows each.
+// Blocks of 128 per round of a wave, for `sets` of 16 weight rows each.
 constexpr int depth(int sets) { return sets <= 2 ? 4 : 2; }
 
 // Expert number `slot` among those with rows, and its rows; false if there are
