@@ -40,8 +40,9 @@ struct Args {
 };
 
 // 32 well mixed bits of an element's number (xor-shift and multiply by odd
-// constants, twice; the constants are primes of a published 32-bit hash); the top 20 of them, and the top 20 of one more product,
-// are the two roundings' random numbers.
+// constants, twice; the constants are primes of a published 32-bit hash); the top
+// 20 of them, and the top 20 of one more product, are the two roundings' random
+// numbers.
 __device__ __forceinline__ uint32_t mix(uint32_t x) {
   x ^= x >> 16;
   x *= 0x9E3779B1u;

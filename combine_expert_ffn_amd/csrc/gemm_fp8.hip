@@ -12,7 +12,8 @@
 // of them become the neighbouring value, which is as near to the unrounded one, and
 // y_p and dx_p are 2.02e-3 and 1.89e-3 from the float64 definition instead of 1.66e-3.
 // With exact products (as for fp16 below) 128 experts of 2048 x 768 take 791 + 432 us
-// forward and 581 + 748 us backward instead of 521 + 287 and 458 + 463.
+// forward and 581 + 748 us backward instead of 521 + 287 and 458 + 463; the 16-bit experts'
+// products take 790 + 468 and 492 + 795.
 // fp16 data, whose results keep 11 bits: the values are widened to bf16 with their
 // scale (exact, one instruction per two) and multiplied by
 // v_mfma_f32_32x32x16_bf16 at half the rate: h 2.07e-4 and y_p 2.2e-4 off, their own rounding.

@@ -524,6 +524,8 @@ int moe_shared_expert_wgrad(const moe_shape* s, int64_t F_s, const void* x, cons
  * rounded up to a multiple of 4; the padding is written as 0).
  *   All calls here need d and F to be multiples of 128 (MOE_ERR_SHAPE); the
  * products need 16-bit data, MOE_BF16 or MOE_F16 (MOE_ERR_UNSUPPORTED).
+ *   q buffers and workspaces are 16-byte aligned, scale buffers 4-byte
+ * (MOE_ERR_ARG).
  *   Sums.  Products of two e4m3 values and their scales are exact, and are
  * summed in float32, where the data is MOE_F16 or there are few rows per expert.
  * MOE_BF16 data with more rows goes through the scaled matrix instruction of
