@@ -19,7 +19,7 @@ from ._lib import (  # noqa: F401
     MOE_STEP_SERIALIZE, MOE_STEP_EAGER_WGRAD, MOE_STEP_SKIP_WGRAD, MOE_STEP_FUSED_PERMUTE,
     MOE_STEP_MID_WGRAD, MOE_STEP_FUSED_COMBINE_BWD, MOE_STEP_PAIR_WGRAD, MOE_STEP_FUSED_SCATTER,
     MOE_STEP_GROUP4_WGRAD, FP8_WEIGHT_FIELDS, MOE_FP8_BLOCK, MoeAdamwHyper, MoeAdamwTensor,
-    MoeFp8Weights,
+    MoeFp8Weights, FP4_WEIGHT_FIELDS, MOE_FP4_BLOCK, MoeFp4Weights,
 )
 
 
@@ -591,6 +591,10 @@ def _chk_fp8(s, fn, q, qs, pair_of_row, offsets, tile_offsets, ws, more):
                            ("pair_of_row", pair_of_row, _I32, cap, True),
                            ("offsets", offsets, _I32, s.E_l + 1, False),
                            ("tile_offsets", tile_offsets, _I32, s.E_l + 1, False)) + more)
+    _chk_ws_on(fn, ws, dev)
+
+
+def _chk_ws_on(fn, ws, dev):
     _chk_ws(fn, ws)
     if ws is not None and ws.get_device() != dev:
         raise MoeError(MOE_ERR_ARG, f"{fn}: ws is on {ws.device}, the current device is cuda:{dev}")
@@ -623,6 +627,115 @@ def moe_ffn_dgrad_fp8(s, dq, ds, pair_of_row, gates, h, offsets, tile_offsets, w
     check(lib().moe_ffn_dgrad_fp8(C.byref(s), _p(dq), _p(ds), _p(pair_of_row), _p(gates), _p(h),
                                   _p(offsets), _p(tile_offsets), w.check(fn, s), _p(dh), _p(dxp),
                                   _p(ag), wp, wb, _stream(stream)))
+
+
+# ---- norm ---------------------------------------------------------------------
+def moe_rmsnorm(s, x, res, gamma, eps, r, y, q, qs, rstd, stream=None):
+    """res, r, y, q (with qs) and rstd may be None; r goes with res, and there is y
+    or q."""
+    fn, n, d = "moe_rmsnorm", s.T * s.d, s.d
+    _chk_all(s, fn, (("x", x, _DATA, n, False), ("res", res, _DATA, n, True),
+                     ("gamma", gamma, _DATA, d, False), ("r", r, _DATA, n, True),
+                     ("y", y, _DATA, n, True), ("q", q, _FP8, n, True),
+                     ("qs", qs, _U8, s.T * ((d // MOE_FP8_BLOCK + 3) // 4 * 4), True),
+                     ("rstd", rstd, _F32, s.T, True)))
+    check(lib().moe_rmsnorm(C.byref(s), _p(x), _p(res), _p(gamma), eps, _p(r), _p(y), _p(q),
+                            _p(qs), _p(rstd), _stream(stream)))
+
+
+def moe_rmsnorm_workspace_bytes(s: MoeShape) -> int:
+    return lib().moe_rmsnorm_workspace_bytes(C.byref(s))
+
+
+def moe_rmsnorm_bwd(s, dy, r, gamma, rstd, dres, dx, dgamma, accumulate, ws, stream=None):
+    """dres and dgamma (with ws) may be None."""
+    fn, n = "moe_rmsnorm_bwd", s.T * s.d
+    dev = _chk_all(s, fn, (("dy", dy, _DATA, n, False), ("r", r, _DATA, n, False),
+                           ("gamma", gamma, _DATA, s.d, False), ("rstd", rstd, _F32, s.T, False),
+                           ("dres", dres, _DATA, n, True), ("dx", dx, _DATA, n, False),
+                           ("dgamma", dgamma, _F32, s.d, True)))
+    _chk_ws_on(fn, ws, dev)
+    wp, wb = _ws(ws)
+    check(lib().moe_rmsnorm_bwd(C.byref(s), _p(dy), _p(r), _p(gamma), _p(rstd), _p(dres), _p(dx),
+                                _p(dgamma), int(accumulate), wp, wb, _stream(stream)))
+
+
+# ---- experts on 4-bit weights ---------------------------------------------------
+class Fp4Weights(_Bound):
+    """The routed experts' weights in 4 bits for shape ``s`` (moe_fp4_weights in
+    include/moe.h): uint8 tensors gu, down (two codes a byte) and their scales gu_s,
+    down_s, allocated here, or all four given.  The tensors are attributes; one that is
+    replaced, or whose memory is, is checked and used from the next call on."""
+
+    def __init__(self, s: MoeShape, device="cuda", **tensors):
+        import torch
+
+        if tensors and set(tensors) != set(FP4_WEIGHT_FIELDS):
+            raise ValueError(f"Fp4Weights: given {sorted(tensors)}, not {FP4_WEIGHT_FIELDS}")
+        self.shape = (s.d, s.F, s.E_l)
+        for name, shape in self._fields().items():
+            t = tensors.get(name)
+            setattr(self, name, torch.empty(shape, dtype=torch.uint8, device=device)
+                    if t is None else t)
+        self._bind()
+
+    def __setattr__(self, name, value):
+        object.__setattr__(self, name, value)
+        if name in FP4_WEIGHT_FIELDS:
+            self._ptrs = None
+
+    def _fields(self):
+        """{name: shape}"""
+        d, F, E_l = self.shape
+        return {"gu": (E_l, 2 * F, d // 2), "gu_s": (E_l, 2 * F, d // MOE_FP4_BLOCK),
+                "down": (E_l, d, F // 2), "down_s": (E_l, d, F // MOE_FP4_BLOCK)}
+
+    def _bind(self):
+        for name, shape in self._fields().items():
+            t = getattr(self, name)
+            _chk(MoeShape(), "Fp4Weights", name, t, _U8, shape[0] * shape[1] * shape[2])
+            if t.device != self.gu.device:
+                raise MoeError(MOE_ERR_ARG, f"Fp4Weights: {name} is on {t.device}, gu on "
+                                            f"{self.gu.device}")
+        self.device = self.gu.get_device()
+        self.struct = MoeFp4Weights(*[_p(getattr(self, n)) for n in FP4_WEIGHT_FIELDS])
+        self._hold(getattr(self, n) for n in FP4_WEIGHT_FIELDS)
+
+    check = Fp8Weights.check
+
+
+def moe_quant_weights_fp4(s, W_gu, W_down, w: Fp4Weights, stream=None):
+    fn, d, F, E_l = "moe_quant_weights_fp4", s.d, s.F, s.E_l
+    _chk_all(s, fn, (("W_gu", W_gu, _DATA, E_l * 2 * F * d, False),
+                     ("W_down", W_down, _DATA, E_l * d * F, False)))
+    check(lib().moe_quant_weights_fp4(C.byref(s), _p(W_gu), _p(W_down), w.check(fn, s),
+                                      _stream(stream)))
+
+
+def moe_dequant_weights_fp4(s, w: Fp4Weights, W_gu, W_down, stream=None):
+    fn, d, F, E_l = "moe_dequant_weights_fp4", s.d, s.F, s.E_l
+    _chk_all(s, fn, (("W_gu", W_gu, _DATA, E_l * 2 * F * d, False),
+                     ("W_down", W_down, _DATA, E_l * d * F, False)))
+    check(lib().moe_dequant_weights_fp4(C.byref(s), w.check(fn, s), _p(W_gu), _p(W_down),
+                                        _stream(stream)))
+
+
+def moe_fp4_workspace_bytes(s: MoeShape) -> int:
+    return lib().moe_fp4_workspace_bytes(C.byref(s))
+
+
+def moe_expert_ffn_fwd_fp4(s, xq, xs, pair_of_row, offsets, tile_offsets, w: Fp4Weights, h, a, yp,
+                           ws, stream=None):
+    """pair_of_row None: xq, xs hold the dispatched rows; else the tokens.  h and
+    a may be None (not written)."""
+    fn, cap, d, F = "moe_expert_ffn_fwd_fp4", s.T * s.K, s.d, s.F
+    _chk_fp8(s, fn, xq, xs, pair_of_row, offsets, tile_offsets, ws,
+             (("h", h, _DATA, cap * 2 * F, True), ("a", a, _DATA, cap * F, True),
+              ("yp", yp, _DATA, cap * d, False)))
+    wp, wb = _ws(ws)
+    check(lib().moe_expert_ffn_fwd_fp4(C.byref(s), _p(xq), _p(xs), _p(pair_of_row), _p(offsets),
+                                       _p(tile_offsets), w.check(fn, s), _p(h), _p(a), _p(yp),
+                                       wp, wb, _stream(stream)))
 
 
 # ---- weight update ----------------------------------------------------------

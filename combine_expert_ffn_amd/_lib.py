@@ -80,6 +80,15 @@ class MoeFp8Weights(C.Structure):
     _fields_ = [(n, C.c_void_p) for n in FP8_WEIGHT_FIELDS]
 
 
+MOE_FP4_BLOCK = 32
+
+FP4_WEIGHT_FIELDS = ["gu", "gu_s", "down", "down_s"]
+
+
+class MoeFp4Weights(C.Structure):
+    _fields_ = [(n, C.c_void_p) for n in FP4_WEIGHT_FIELDS]
+
+
 class MoeAdamwTensor(C.Structure):
     _fields_ = [("n", C.c_int64)] + [(n, C.c_void_p) for n in ("param", "master", "grad", "m", "v",
                                                                "m_s", "v_s")] + [
@@ -97,6 +106,7 @@ class MoeAdamwHyper(C.Structure):
 _P = C.c_void_p
 _SP = C.POINTER(MoeShape)
 _WP = C.POINTER(MoeFp8Weights)
+_WP4 = C.POINTER(MoeFp4Weights)
 SIGNATURES = {
     "moe_workspace_bytes": (C.c_size_t, [_SP]),
     "moe_step_workspace_bytes": (C.c_size_t, [_SP]),
@@ -143,6 +153,14 @@ SIGNATURES = {
                                          _P]),
     "moe_ffn_dgrad_fp8": (C.c_int, [_SP, _P, _P, _P, _P, _P, _P, _P, _WP, _P, _P, _P, _P,
                                     C.c_size_t, _P]),
+    "moe_rmsnorm": (C.c_int, [_SP, _P, _P, _P, C.c_float, _P, _P, _P, _P, _P, _P]),
+    "moe_rmsnorm_workspace_bytes": (C.c_size_t, [_SP]),
+    "moe_rmsnorm_bwd": (C.c_int, [_SP, _P, _P, _P, _P, _P, _P, _P, C.c_int, _P, C.c_size_t, _P]),
+    "moe_quant_weights_fp4": (C.c_int, [_SP, _P, _P, _WP4, _P]),
+    "moe_dequant_weights_fp4": (C.c_int, [_SP, _WP4, _P, _P, _P]),
+    "moe_fp4_workspace_bytes": (C.c_size_t, [_SP]),
+    "moe_expert_ffn_fwd_fp4": (C.c_int, [_SP, _P, _P, _P, _P, _P, _WP4, _P, _P, _P, _P, C.c_size_t,
+                                         _P]),
     "moe_adamw": (C.c_int, [C.POINTER(MoeAdamwTensor), C.c_int, C.POINTER(MoeAdamwHyper), _P]),
     "moe_overlap_step": (C.c_int, [C.POINTER(MoeStep), _P, _P, C.c_int]),
     "moe_overlap_steps": (C.c_int, [C.POINTER(MoeStep), C.c_int, _P, _P, C.c_int]),

@@ -619,6 +619,105 @@ int moe_ffn_dgrad_fp8(const moe_shape* s, const void* dq, const uint8_t* ds,
                       const moe_fp8_weights* w, void* dh, void* dxp, void* ag, void* ws,
                       size_t ws_bytes, hipStream_t stream);
 
+/* ---- norm ------------------------------------------------------------------- */
+/*
+ * moe_rmsnorm - the root-mean-square norm in front of the layer, with the addition
+ * of the residual stream before it and the 8-bit rows of the experts behind it:
+ *   r = x + res (rounded to dtype; r = x with res NULL)
+ *   rstd = 1 / sqrt(mean(r^2) + eps);  y = r * rstd * gamma (rounded to dtype)
+ *   q, qs: y quantised, bit for bit as moe_quant_rows_fp8 quantises it
+ *   x [T,d], res [T,d] or NULL, gamma [d] (dtype)
+ *   r [T,d] out (dtype) or NULL; only with res (without, r is x: MOE_ERR_ARG)
+ *   y [T,d] out (dtype) or NULL; q [T,d] e4m3 and qs [T,ld(d)] out, or both NULL;
+ *   at least one of y and q (MOE_ERR_NULL)
+ *   rstd [T] f32 out or NULL: what the backward needs
+ * Sums are float32 (rows with values past 1e17 are summed in units of 2^80, so none
+ * overflows).  A value that is not finite reaches its own row alone (NaN: all of it; an
+ * infinity: NaN in its place, 0 elsewhere).
+ *   r and y may be x or res themselves (element for element); two outputs may not
+ * share memory.
+ *   eps finite, at least 1e-30 (MOE_ERR_ARG: below, float32 squares would lose digits);
+ * q needs d to be a multiple of 128 (MOE_ERR_SHAPE).
+ * All pointers 16-byte aligned but qs and rstd, which are 4-byte (MOE_ERR_ARG).  With
+ * T = 0 nothing is done and the row pointers may be NULL (so in the backward pass too).
+ * Of the shape, F, E, e_lo, E_l and K are checked and not used.
+ */
+int moe_rmsnorm(const moe_shape* s, const void* x, const void* res, const void* gamma, float eps,
+                void* r, void* y, void* q, uint8_t* qs, float* rstd, hipStream_t stream);
+
+/* Bytes of workspace moe_rmsnorm_bwd needs; they never fall as T grows. */
+size_t moe_rmsnorm_workspace_bytes(const moe_shape* s);
+
+/*
+ * moe_rmsnorm_bwd - its backward pass for the gradient dy [T,d] of y (of the
+ * quantised y too, whose rounding is passed straight through).  With xhat = r * rstd and
+ * dn = dy * gamma:
+ *   dx = rstd * (dn - xhat * mean(dn * xhat)) [+ dres]   (one rounding)
+ *   dgamma[j] = sum_t dy[t,j] * xhat[t,j]
+ * dx is the gradient of x and of res alike; dres [T,d] (dtype) or NULL is the
+ * gradient that reaches r past the norm (the residual stream's).
+ *   r [T,d] (x where there was no res), rstd [T] f32 from moe_rmsnorm
+ *   dx [T,d] out (dtype); may be dy, dres or r itself
+ *   dgamma [d] f32 out or NULL (ws may then be NULL); accumulate & MOE_ACCUM_DW adds
+ *   to the existing values, otherwise T = 0 gives 0.  Summed in a fixed order.
+ * Alignment as moe_rmsnorm; dgamma and ws 16-byte.
+ */
+int moe_rmsnorm_bwd(const moe_shape* s, const void* dy, const void* r, const void* gamma,
+                    const float* rstd, const void* dres, void* dx, float* dgamma, int accumulate,
+                    void* ws, size_t ws_bytes, hipStream_t stream);
+
+/* ---- experts on 4-bit weights ------------------------------------------------- */
+/*
+ * The routed experts' weights in 4 bits: e2m1 codes (bit 3 the sign; magnitudes 0,
+ * 0.5, 1, 1.5, 2, 3, 4, 6 for the codes 0 .. 7), two per byte along the product's
+ * reduction axis, the first in the low half, and one scale byte s per block of
+ * MOE_FP4_BLOCK values along it: a code stands for value * 2^(s - 127), 0 <= s <= 254,
+ * and every code of a block with s = 255 for NaN.  This is the microscaled 4-bit
+ * format of the Open Compute Project, so weights quantised elsewhere can be used too.
+ *   moe_quant_weights_fp4 takes the smallest power of two with max|x| <= 7 * scale (127
+ * for a block of zeros, never below 0) and rounds x / scale to nearest even, up to 7
+ * to 6: 6 is the nearest code as long as it has no larger neighbour at 8 (on normal
+ * values the error is 0.1119 of the values, rms; 0.1154 where the scale doubles past 6
+ * already, 0.1150 where it doubles past 8).  A block with a value that is not finite gets
+ * s = 255 and codes 0.
+ *   All calls here need d and F to be multiples of 128 (MOE_ERR_SHAPE).  Codes are
+ * 16-byte aligned, scales 4-byte (MOE_ERR_ARG).
+ */
+#define MOE_FP4_BLOCK 32
+
+typedef struct moe_fp4_weights {
+  uint8_t* gu;       /* [E_l,2F,d/2]   W_gu            */
+  uint8_t* gu_s;     /* [E_l,2F,d/32]                  */
+  uint8_t* down;     /* [E_l,d,F/2]    W_down          */
+  uint8_t* down_s;   /* [E_l,d,F/32]                   */
+} moe_fp4_weights;
+
+/* moe_quant_weights_fp4 - quantise W_gu [E_l,2F,d] and W_down [E_l,d,F] (dtype, any of
+ * the three, 16-byte aligned) into w. */
+int moe_quant_weights_fp4(const moe_shape* s, const void* W_gu, const void* W_down,
+                          const moe_fp4_weights* w, hipStream_t stream);
+
+/* moe_dequant_weights_fp4 - the values that w stands for, rounded to dtype: exact in
+ * MOE_F32, and in the 16-bit types within their range.  moe_ffn_dgrad on them is the
+ * gradient of moe_expert_ffn_fwd_fp4 (the quantisation of rows passed straight through). */
+int moe_dequant_weights_fp4(const moe_shape* s, const moe_fp4_weights* w, void* W_gu,
+                            void* W_down, hipStream_t stream);
+
+/* Bytes of workspace moe_expert_ffn_fwd_fp4 needs; they never fall as T grows. */
+size_t moe_fp4_workspace_bytes(const moe_shape* s);
+
+/*
+ * moe_expert_ffn_fwd_fp4 - moe_expert_ffn_fwd_fp8 with the weights in 4 bits: 8-bit rows
+ * (moe_quant_rows_fp8, moe_rmsnorm) on 4-bit weights, a quantised to 8 bits between
+ * the two products.  Arguments, sums and rows >= N as there; w as above.  With T = 0
+ * nothing is done and the other pointers may be NULL.
+ *   ws: moe_fp4_workspace_bytes.
+ */
+int moe_expert_ffn_fwd_fp4(const moe_shape* s, const void* xq, const uint8_t* xs,
+                           const int32_t* pair_of_row, const int32_t* offsets,
+                           const int32_t* tile_offsets, const moe_fp4_weights* w, void* h,
+                           void* a, void* yp, void* ws, size_t ws_bytes, hipStream_t stream);
+
 /* ---- weight update --------------------------------------------------------- */
 /*
  * One tensor of an AdamW step (device pointers).  The state is float32, or, with
