@@ -20,7 +20,8 @@ BUILD_DIR = os.path.join(ROOT, "_build")
 LIB = os.path.join(HERE, "libmoe.so")
 SOURCES = ["abi.cpp", "route.hip", "dispatch.hip", "gemm_mfma.hip", "gemm_simt.hip",
            "abi_fp8.cpp", "quant_fp8.hip", "gemm_fp8.hip", "gemm_fp8_small.hip",
-           "adamw.hip", "abi_norm_fp4.cpp", "norm.hip", "quant_fp4.hip", "gemm_fp4_small.hip"]
+           "adamw.hip", "abi_norm_fp4.cpp", "norm.hip", "quant_fp4.hip", "gemm_fp4.hip",
+           "gemm_fp4_small.hip"]
 
 
 def hipcc() -> str:

@@ -197,15 +197,25 @@ int ffn_fwd_t(const moe_shape* s, const void* xq, const uint8_t* xs, const int32
 
 }  // namespace
 
-size_t fp4_workspace_bytes(const moe_shape* s) {
-  const size_t b = align_up((size_t)(s->T * s->K * s->F) * sizeof(float), 256);
-  return b < 256 ? 256 : b;
+// Few rows: see fp8_small; the same form.
+static int64_t most_mean(const moe_shape* s) {
+  const int64_t most = s->dtype == MOE_BF16 ? 800000000 : 1400000000;
+  return std::min<int64_t>(256, 11 + most / (s->E_l * s->F * s->d));
+}
+bool fp4_small(const moe_shape* s) {
+  return cdiv(s->T * s->K, s->E) <= most_mean(s) &&
+         std::max(Shape(s, (int)s->F, false).passes, Shape(s, (int)s->d, true).passes) <= 8;
+}
+// For the longest batch of at most T tokens that these kernels take.
+size_t fp4_small_workspace_bytes(const moe_shape* s) {
+  const int64_t rows = std::min(s->T * s->K, s->E * most_mean(s));
+  return (size_t)(rows * s->F) * sizeof(float);
 }
 
-int launch_ffn_fwd_fp4(const moe_shape* s, const void* xq, const uint8_t* xs,
-                       const int32_t* xrows, const int32_t* offsets,
-                       const int32_t* tile_offsets, const moe_fp4_weights* w, void* h, void* a,
-                       void* yp, void* ws, hipStream_t st) {
+int launch_ffn_fwd_fp4_small(const moe_shape* s, const void* xq, const uint8_t* xs,
+                             const int32_t* xrows, const int32_t* offsets,
+                             const moe_fp4_weights* w, void* h, void* a, void* yp, void* ws,
+                             hipStream_t st) {
   return s->dtype == MOE_BF16
              ? ffn_fwd_t<uint16_t>(s, xq, xs, xrows, offsets, w, h, a, yp, ws, st)
              : ffn_fwd_t<_Float16>(s, xq, xs, xrows, offsets, w, h, a, yp, ws, st);

@@ -32,5 +32,12 @@ int launch_ffn_fwd_fp4(const moe_shape* s, const void* xq, const uint8_t* xs,
                        const int32_t* xrows, const int32_t* offsets,
                        const int32_t* tile_offsets, const moe_fp4_weights* w, void* h, void* a,
                        void* yp, void* ws, hipStream_t st);
+// The same for few rows per expert (gemm_fp4_small.hip), and the rule that takes it.
+bool fp4_small(const moe_shape* s);
+size_t fp4_small_workspace_bytes(const moe_shape* s);
+int launch_ffn_fwd_fp4_small(const moe_shape* s, const void* xq, const uint8_t* xs,
+                             const int32_t* xrows, const int32_t* offsets,
+                             const moe_fp4_weights* w, void* h, void* a, void* yp, void* ws,
+                             hipStream_t st);
 
 }  // namespace moe
