@@ -19,6 +19,14 @@
 namespace moe {
 namespace {
 
+// As stage_wait(), as a wait that the compiler sees: behind the inline assembly it would
+// wait again ahead of each use of the fetched scales, for the copies of the next stage too.
+__device__ __forceinline__ void all_here() {
+  asm volatile("" : : : "memory");
+  __builtin_amdgcn_s_waitcnt(0x0f70);  // vmcnt(0) alone
+  asm volatile("" : : : "memory");
+}
+
 __device__ __forceinline__ uint32_t scalar(uint32_t v) {
   return (uint32_t)__builtin_amdgcn_readfirstlane((int)v);
 }
@@ -137,12 +145,14 @@ __device__ __forceinline__ i32x4_t weight_frag(const uint8_t* tile, int row0, in
 // One 64-deep slice (CUR of its stage): the MFMAs of the wave on a and b, and beside them
 // the reads of the next slice's fragments: rows from na, slice 1 - CUR of their stage,
 // weights from nb, slice nq of their two stages.  sb: the weight scales, already
-// shifted by the lane's half.
-template <bool WIDE, int CUR>
+// shifted by the lane's half.  between(j) is what else is issued behind the MFMAs of
+// column tile j: they keep the matrix core busy meanwhile, where ahead of them, behind a
+// barrier, it would stand idle.
+template <bool WIDE, int CUR, class Between>
 __device__ __forceinline__ void slice(const i32x8_t (&a)[TM], i32x8_t (&an)[TM], i32x4_t (&b)[TN],
                                       const uint32_t (&sa)[TM], const uint32_t (&sb)[TN],
                                       f32x16_t (&acc)[TM][TN], const uint8_t* na,
-                                      const uint8_t* nb, int nq, const Pos& w) {
+                                      const uint8_t* nb, int nq, const Pos& w, Between between) {
   auto next_b = [&](int j) { return weight_frag(nb, w.wn * WTN + j * 32, nq, w.lane); };
   auto next_a = [&]() {
 #pragma unroll
@@ -167,6 +177,7 @@ __device__ __forceinline__ void slice(const i32x8_t (&a)[TM], i32x8_t (&an)[TM],
         for (int i = 0; i < TM; ++i)
           acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(aw[i], bw, acc[i][j], 0, 0, 0);
         if (q == 3) b[j] = next_b(j);
+        if (q == 0) between(j);
         __builtin_amdgcn_sched_barrier(0);
       }
     }
@@ -182,6 +193,7 @@ __device__ __forceinline__ void slice(const i32x8_t (&a)[TM], i32x8_t (&an)[TM],
       for (int i = 0; i < TM; ++i)  // 0: e4m3, 4: e2m1
         acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
             a[i], bw, acc[i][j], 0, 4, 0, (int)sa[i], 2 * CUR, (int)sb[j]);
+      between(j);
       __builtin_amdgcn_sched_barrier(0);
     }
 #pragma unroll
@@ -208,20 +220,23 @@ __device__ __forceinline__ void mainloop(const Load& la, const Load4& lb, Scales
   int kb = k0;                        // the stage's block of the reduction
   int kc = after(after(k0, nk), nk);  // the block of the stage that is copied next
   int kn = kc;                        // the first block of the pair that is copied next
-  auto copies = [&](int kt) {
+  auto copy_a = [&](int kt) {
+    la.copy(kc, lds + (kt & 1) * 2 * STAGE, kt + 2 < nk, below);
+    kc = after(kc, nk);
+  };
+  auto copy_b = [&](int kt) {
     const int odd = kt & 1, pair = (kt >> 1) + 1 + odd;
-    la.copy(kc, lds + odd * 2 * STAGE, kt + 2 < nk, below);
     lb.copy(kn, nk, odd, lds + STAGE + (pair & 1) * 2 * STAGE, 2 * pair < nk);
     if (!odd) kn = after(after(kn, nk), nk);
-    kc = after(kc, nk);
   };
   if (idle) {  // wave-uniform: only its part of the copies, and the barriers
     for (int kt = 0; kt < nk; ++kt) {
-      stage_wait();
+      all_here();
       __syncthreads();
-      copies(kt);
+      copy_a(kt);
+      copy_b(kt);
     }
-    stage_wait();
+    all_here();
     __syncthreads();
     return;
   }
@@ -235,7 +250,7 @@ __device__ __forceinline__ void mainloop(const Load& la, const Load4& lb, Scales
   for (int kt = 0; kt < nk;) {
     // the stages whose scales were fetched together
     const int end = min(kt + min(4 - (kb & 3), nk - kb), nk);
-    for (; kt < end; ++kt, ++kb) {
+    do {
       const int odd = kt & 1;
       const uint8_t* cur = smem + odd * 2 * STAGE;
       const uint8_t* nxt = smem + (odd ^ 1) * 2 * STAGE;
@@ -247,20 +262,23 @@ __device__ __forceinline__ void mainloop(const Load& la, const Load4& lb, Scales
       for (int i = 0; i < TM; ++i) sa[i] = sc.a[i] >> sh;
       sc.step(half, sb);
       __builtin_amdgcn_sched_barrier(0);
-      slice<WIDE, 0>(a0, a1, b, sa, sb, acc, cur, wcur, odd * 2 + 1, w);
-      stage_wait();
+      slice<WIDE, 0>(a0, a1, b, sa, sb, acc, cur, wcur, odd * 2 + 1, w, [](int) {});
+      all_here();
       __syncthreads();
-      copies(kt);
       __builtin_amdgcn_sched_barrier(0);
-      slice<WIDE, 1>(a1, a0, b, sa, sb, acc, nxt, wnxt, (odd ^ 1) * 2, w);
-    }
+      slice<WIDE, 1>(a1, a0, b, sa, sb, acc, nxt, wnxt, (odd ^ 1) * 2, w, [&](int j) {
+        if (j == 0) copy_a(kt);
+        if (j == 1) copy_b(kt);
+      });
+      ++kb;
+    } while (++kt < end);
     if (kb == nk) kb = 0;
     sc.next();
     __builtin_amdgcn_sched_barrier(0);
     sc.fetch((kb | 3) + 1 < nk ? (kb | 3) + 1 : 0, sc.an, sc.bn);
     __builtin_amdgcn_sched_barrier(0);
   }
-  stage_wait();  // the copies past the last stage write zeros to LDS
+  all_here();  // the copies past the last stage write zeros to LDS
   __syncthreads();
 }
 
@@ -373,7 +391,7 @@ __global__ __launch_bounds__(NT) void fp4_kernel(Op op, const int32_t* __restric
   };
   // The next tile's first stage and scales are here, ahead of this one's stores.
   auto arrived = [&]() {
-    stage_wait();
+    all_here();
     sc.arrived(k0);
   };
   if (!locate()) return;
