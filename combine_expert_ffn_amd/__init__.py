@@ -471,6 +471,32 @@ def _chk_all(s, fn, tensors):
     return dev
 
 
+def _args(s, fn, tensors):
+    """_chk_all, and with it the tensors' addresses (None for None)."""
+    import torch
+
+    if not _DTYPES:
+        _chk_all(s, fn, ())
+    want = _DTYPES.get(s.dtype) or {}
+    dev = torch._C._cuda_getDevice() if torch.cuda.is_initialized() else -2
+    out = []
+    try:
+        for name, t, kind, numel, optional in tensors:
+            if t is None and optional:
+                out.append(None)
+            elif (t.dtype is want.get(kind) and t.get_device() == dev and t.is_contiguous()
+                  and t.numel() >= numel):
+                out.append(t.data_ptr() or _p(t))
+            else:
+                break
+        else:
+            return out
+    except AttributeError:      # not a tensor
+        pass
+    _chk_all(s, fn, tensors)    # raises what is wrong
+    raise MoeError(MOE_ERR_ARG, f"{fn}: a tensor argument does not fit the shape")
+
+
 class _Bound:
     """Tensors whose addresses a C struct holds between calls.  They are compared on
     every call (0.08 us each), and bound and checked again where one has moved
@@ -591,10 +617,6 @@ def _chk_fp8(s, fn, q, qs, pair_of_row, offsets, tile_offsets, ws, more):
                            ("pair_of_row", pair_of_row, _I32, cap, True),
                            ("offsets", offsets, _I32, s.E_l + 1, False),
                            ("tile_offsets", tile_offsets, _I32, s.E_l + 1, False)) + more)
-    _chk_ws_on(fn, ws, dev)
-
-
-def _chk_ws_on(fn, ws, dev):
     _chk_ws(fn, ws)
     if ws is not None and ws.get_device() != dev:
         raise MoeError(MOE_ERR_ARG, f"{fn}: ws is on {ws.device}, the current device is cuda:{dev}")
@@ -630,17 +652,30 @@ def moe_ffn_dgrad_fp8(s, dq, ds, pair_of_row, gates, h, offsets, tile_offsets, w
 
 
 # ---- norm ---------------------------------------------------------------------
+def _ws_on(fn, ws):
+    """_ws, on the current device."""
+    import torch
+
+    if ws is None:
+        return None, 0
+    _chk_ws(fn, ws)
+    if ws.get_device() != torch.cuda.current_device():
+        raise MoeError(MOE_ERR_ARG, f"{fn}: ws is on {ws.device}, the current device is "
+                                    f"cuda:{torch.cuda.current_device()}")
+    return ws.data_ptr(), ws.numel() * ws.element_size()
+
+
 def moe_rmsnorm(s, x, res, gamma, eps, r, y, q, qs, rstd, stream=None):
     """res, r, y, q (with qs) and rstd may be None; r goes with res, and there is y
     or q."""
-    fn, n, d = "moe_rmsnorm", s.T * s.d, s.d
-    _chk_all(s, fn, (("x", x, _DATA, n, False), ("res", res, _DATA, n, True),
-                     ("gamma", gamma, _DATA, d, False), ("r", r, _DATA, n, True),
-                     ("y", y, _DATA, n, True), ("q", q, _FP8, n, True),
-                     ("qs", qs, _U8, s.T * ((d // MOE_FP8_BLOCK + 3) // 4 * 4), True),
-                     ("rstd", rstd, _F32, s.T, True)))
-    check(lib().moe_rmsnorm(C.byref(s), _p(x), _p(res), _p(gamma), eps, _p(r), _p(y), _p(q),
-                            _p(qs), _p(rstd), _stream(stream)))
+    T, d = s.T, s.d
+    n = T * d
+    x, res, gamma, r, y, q, qs, rstd = _args(s, "moe_rmsnorm", (
+        ("x", x, _DATA, n, False), ("res", res, _DATA, n, True), ("gamma", gamma, _DATA, d, False),
+        ("r", r, _DATA, n, True), ("y", y, _DATA, n, True), ("q", q, _FP8, n, True),
+        ("qs", qs, _U8, T * ((d // MOE_FP8_BLOCK + 3) // 4 * 4), True),
+        ("rstd", rstd, _F32, T, True)))
+    check(lib().moe_rmsnorm(s, x, res, gamma, eps, r, y, q, qs, rstd, _stream(stream)))
 
 
 def moe_rmsnorm_workspace_bytes(s: MoeShape) -> int:
@@ -649,15 +684,15 @@ def moe_rmsnorm_workspace_bytes(s: MoeShape) -> int:
 
 def moe_rmsnorm_bwd(s, dy, r, gamma, rstd, dres, dx, dgamma, accumulate, ws, stream=None):
     """dres and dgamma (with ws) may be None."""
-    fn, n = "moe_rmsnorm_bwd", s.T * s.d
-    dev = _chk_all(s, fn, (("dy", dy, _DATA, n, False), ("r", r, _DATA, n, False),
-                           ("gamma", gamma, _DATA, s.d, False), ("rstd", rstd, _F32, s.T, False),
-                           ("dres", dres, _DATA, n, True), ("dx", dx, _DATA, n, False),
-                           ("dgamma", dgamma, _F32, s.d, True)))
-    _chk_ws_on(fn, ws, dev)
-    wp, wb = _ws(ws)
-    check(lib().moe_rmsnorm_bwd(C.byref(s), _p(dy), _p(r), _p(gamma), _p(rstd), _p(dres), _p(dx),
-                                _p(dgamma), int(accumulate), wp, wb, _stream(stream)))
+    fn, d = "moe_rmsnorm_bwd", s.d
+    n = s.T * d
+    dy, r, gamma, rstd, dres, dx, dgamma = _args(s, fn, (
+        ("dy", dy, _DATA, n, False), ("r", r, _DATA, n, False), ("gamma", gamma, _DATA, d, False),
+        ("rstd", rstd, _F32, s.T, False), ("dres", dres, _DATA, n, True),
+        ("dx", dx, _DATA, n, False), ("dgamma", dgamma, _F32, d, True)))
+    wp, wb = _ws_on(fn, ws)
+    check(lib().moe_rmsnorm_bwd(s, dy, r, gamma, rstd, dres, dx, dgamma, int(accumulate), wp, wb,
+                                _stream(stream)))
 
 
 # ---- experts on 4-bit weights ---------------------------------------------------
@@ -704,20 +739,21 @@ class Fp4Weights(_Bound):
     check = Fp8Weights.check
 
 
+def _fp4_matrices(s, fn, W_gu, W_down):
+    n = s.E_l * s.F * s.d
+    return _args(s, fn, (("W_gu", W_gu, _DATA, 2 * n, False), ("W_down", W_down, _DATA, n, False)))
+
+
 def moe_quant_weights_fp4(s, W_gu, W_down, w: Fp4Weights, stream=None):
-    fn, d, F, E_l = "moe_quant_weights_fp4", s.d, s.F, s.E_l
-    _chk_all(s, fn, (("W_gu", W_gu, _DATA, E_l * 2 * F * d, False),
-                     ("W_down", W_down, _DATA, E_l * d * F, False)))
-    check(lib().moe_quant_weights_fp4(C.byref(s), _p(W_gu), _p(W_down), w.check(fn, s),
-                                      _stream(stream)))
+    fn = "moe_quant_weights_fp4"
+    W_gu, W_down = _fp4_matrices(s, fn, W_gu, W_down)
+    check(lib().moe_quant_weights_fp4(s, W_gu, W_down, w.check(fn, s), _stream(stream)))
 
 
 def moe_dequant_weights_fp4(s, w: Fp4Weights, W_gu, W_down, stream=None):
-    fn, d, F, E_l = "moe_dequant_weights_fp4", s.d, s.F, s.E_l
-    _chk_all(s, fn, (("W_gu", W_gu, _DATA, E_l * 2 * F * d, False),
-                     ("W_down", W_down, _DATA, E_l * d * F, False)))
-    check(lib().moe_dequant_weights_fp4(C.byref(s), w.check(fn, s), _p(W_gu), _p(W_down),
-                                        _stream(stream)))
+    fn = "moe_dequant_weights_fp4"
+    W_gu, W_down = _fp4_matrices(s, fn, W_gu, W_down)
+    check(lib().moe_dequant_weights_fp4(s, w.check(fn, s), W_gu, W_down, _stream(stream)))
 
 
 def moe_fp4_workspace_bytes(s: MoeShape) -> int:
@@ -728,14 +764,18 @@ def moe_expert_ffn_fwd_fp4(s, xq, xs, pair_of_row, offsets, tile_offsets, w: Fp4
                            ws, stream=None):
     """pair_of_row None: xq, xs hold the dispatched rows; else the tokens.  h and
     a may be None (not written)."""
-    fn, cap, d, F = "moe_expert_ffn_fwd_fp4", s.T * s.K, s.d, s.F
-    _chk_fp8(s, fn, xq, xs, pair_of_row, offsets, tile_offsets, ws,
-             (("h", h, _DATA, cap * 2 * F, True), ("a", a, _DATA, cap * F, True),
-              ("yp", yp, _DATA, cap * d, False)))
-    wp, wb = _ws(ws)
-    check(lib().moe_expert_ffn_fwd_fp4(C.byref(s), _p(xq), _p(xs), _p(pair_of_row), _p(offsets),
-                                       _p(tile_offsets), w.check(fn, s), _p(h), _p(a), _p(yp),
-                                       wp, wb, _stream(stream)))
+    fn, T, d, F, n = "moe_expert_ffn_fwd_fp4", s.T, s.d, s.F, s.E_l + 1
+    cap = T * s.K
+    rows = cap if pair_of_row is None else T
+    xq, xs, pair_of_row, offsets, tile_offsets, h, a, yp = _args(s, fn, (
+        ("xq", xq, _FP8, rows * d, False),
+        ("xs", xs, _U8, rows * ((d // MOE_FP8_BLOCK + 3) // 4 * 4), False),
+        ("pair_of_row", pair_of_row, _I32, cap, True), ("offsets", offsets, _I32, n, False),
+        ("tile_offsets", tile_offsets, _I32, n, False), ("h", h, _DATA, cap * 2 * F, True),
+        ("a", a, _DATA, cap * F, True), ("yp", yp, _DATA, cap * d, False)))
+    wp, wb = _ws_on(fn, ws)
+    check(lib().moe_expert_ffn_fwd_fp4(s, xq, xs, pair_of_row, offsets, tile_offsets,
+                                       w.check(fn, s), h, a, yp, wp, wb, _stream(stream)))
 
 
 # ---- weight update ----------------------------------------------------------

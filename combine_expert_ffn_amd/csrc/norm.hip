@@ -268,17 +268,25 @@ __global__ __launch_bounds__(NT) void rmsnorm_bwd_kernel(Bwd<T> a) {
   }
 }
 
-// dgamma from n rows of partial sums: 16 columns to a block, 16 threads to a column.
-__global__ __launch_bounds__(NT) void rmsnorm_dgamma_kernel(const float* __restrict__ parts, int n,
-                                                            int d, bool accumulate,
-                                                            float* __restrict__ dgamma) {
-  __shared__ float s[16][17];
+// dgamma from n rows of partial sums: 16 columns to a block, 64 threads to a column, each
+// with eight rows in flight.
+__global__ __launch_bounds__(1024) void rmsnorm_dgamma_kernel(const float* __restrict__ parts,
+                                                              int n, int d, bool accumulate,
+                                                              float* __restrict__ dgamma) {
+  __shared__ float s[16][16];
   const int col = threadIdx.x & 15, grp = threadIdx.x >> 4, j = blockIdx.x * 16 + col;
   float v = 0.f;
-  for (int i = grp; i < n; i += 16) v += parts[(size_t)i * d + j];
-  s[grp][col] = v;
+  for (int i = grp; i < n; i += 512) {
+    float f[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) f[k] = i + k * 64 < n ? parts[(size_t)(i + k * 64) * d + j] : 0.f;
+    v += ((f[0] + f[1]) + (f[2] + f[3])) + ((f[4] + f[5]) + (f[6] + f[7]));
+  }
+  v += __shfl_xor(v, 16, 64);
+  v += __shfl_xor(v, 32, 64);
+  if ((threadIdx.x & 63) < 16) s[threadIdx.x >> 6][col] = v;
   __syncthreads();
-  if (grp == 0) {
+  if (threadIdx.x < 16) {
     float t = 0.f;
 #pragma unroll
     for (int i = 0; i < 16; ++i) t += s[i][col];
@@ -347,7 +355,7 @@ int rmsnorm_bwd_t(const moe_shape* s, const void* dy, const void* r, const void*
   }
   if (!dgamma) return MOE_OK;
   MOE_LAUNCH("rmsnorm_dgamma", st,
-             rmsnorm_dgamma_kernel<<<(int)(s->d / 16), NT, 0, st>>>(parts, n, (int)s->d, accumulate,
+             rmsnorm_dgamma_kernel<<<(int)(s->d / 16), 1024, 0, st>>>(parts, n, (int)s->d, accumulate,
                                                                     dgamma));
   return check_launch("rmsnorm_dgamma");
 }
