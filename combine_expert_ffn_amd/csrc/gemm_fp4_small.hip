@@ -347,10 +347,21 @@ int launch(const char* name, const moe_shape* s, const Op& op, const WRows4& W, 
   };
   auto by_rows = [&](auto S_) {
     constexpr int S = decltype(S_)::value;
-    if (sh.G == 4) return go(fp4_small_kernel<S, 4, 0, Op>);
-    if (sh.G == 2) return go(fp4_small_kernel<S, 2, 0, Op>);
-    if (per_wave > 2 || W.k == 128) return go(fp4_small_kernel<S, 1, 0, Op>);
-    return per_wave == 1 ? go(fp4_small_kernel<S, 1, 1, Op>) : go(fp4_small_kernel<S, 1, 2, Op>);
+    // as many units' rows in registers as leave two waves to a SIMD
+    auto by_units = [&](auto G_, auto most) {
+      constexpr int G = decltype(G_)::value, MOST = decltype(most)::value;
+      if (per_wave > MOST || W.k == 128) return go(fp4_small_kernel<S, G, 0, Op>);
+      if constexpr (MOST == 2)
+        if (per_wave == 2) return go(fp4_small_kernel<S, G, 2, Op>);
+      return go(fp4_small_kernel<S, G, 1, Op>);
+    };
+    typedef std::integral_constant<int, 1> One;
+    typedef std::integral_constant<int, 2> Two;
+    if (sh.G == 4)
+      return by_units(std::integral_constant<int, 4>{},
+                      std::integral_constant<int, Op::WIDE || S == 4 ? 1 : 2>{});
+    if (sh.G == 2) return by_units(Two{}, std::integral_constant<int, Op::WIDE ? 1 : 2>{});
+    return by_units(One{}, Two{});
   };
   if constexpr (Op::H == 1)
     if (sh.S == 4) return by_rows(std::integral_constant<int, 4>{});
@@ -373,10 +384,22 @@ int ffn_fwd_t(const moe_shape* s, const void* xq, const uint8_t* xs, const int32
 
 }  // namespace
 
-// Few rows: see fp8_small; the same form.
+// Few rows: up to 20 per expert on average (17 in fp16), and (x / E_l F d)^2 more with x =
+// 5e7 in bf16 and 7e7 in fp16, 256 at most.  Below it these kernels are faster than the tiles,
+// whose time hardly falls with the rows; above, more than 32 rows of an expert take a pass
+// over its weights each, or more registers than leave two waves to a SIMD.  Both sides in us
+// on an MI355X, forward, small against tiles: bf16, 128 experts of 2048 x 768 at 8 rows 88 / 121,
+// at 16 96 / 121, at 20 124 / 122, at 24 146 / 123; 64 of them at 20 62 / 76, at 24 84 / 75; 16 of
+// 4096 x 1024 at 20 53 / 60, at 25 68 / 60; 8 of 2048 x 1408 at 21 25 / 37, at 26 50 / 37; 8 of
+// 2048 x 768 at 32 23 / 32, at 64 29 / 33; 4 of 640 x 384 at 256 15 / 26, at 400 29 / 23.  fp16: 128
+// of 2048 x 768 at 16 136 / 151, at 20 183 / 152; 8 of 2048 x 1408 at 21 39 / 54, at 26 58 / 55; 8 of
+// 2048 x 768 at 64 40 / 49, at 128 67 / 50.
+// As for the 8-bit kernels, no block may need more than 8 passes with every token on one
+// expert.
 static int64_t most_mean(const moe_shape* s) {
-  const int64_t most = s->dtype == MOE_BF16 ? 800000000 : 1400000000;
-  return std::min<int64_t>(256, 11 + most / (s->E_l * s->F * s->d));
+  const bool bf16 = s->dtype == MOE_BF16;
+  const double more = (bf16 ? 5e7 : 7e7) / ((double)s->E_l * (double)s->F * (double)s->d);
+  return std::min<int64_t>(256, (bf16 ? 20 : 17) + (int64_t)std::min(256.0, more * more));
 }
 bool fp4_small(const moe_shape* s) {
   return cdiv(s->T * s->K, s->E) <= most_mean(s) &&
