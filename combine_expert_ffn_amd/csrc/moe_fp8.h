@@ -72,6 +72,22 @@ __device__ __forceinline__ bf16x8_t widen(int lo, int hi, float scale) {
   return bf16x8_t{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
 }
 
+// Loads and stores of N words, with PAST past the caches (non-temporal): for data of
+// which no cache holds the beginning when the end is reached.
+template <int N, bool PAST>
+struct Words {
+  typedef uint32_t type __attribute__((ext_vector_type(N)));
+  static __device__ __forceinline__ type load(const void* p) {
+    return PAST ? __builtin_nontemporal_load((const type*)p) : *(const type*)p;
+  }
+  static __device__ __forceinline__ void store(void* p, type v) {
+    if constexpr (PAST) __builtin_nontemporal_store(v, (type*)p);
+    else *(type*)p = v;
+  }
+};
+// The size from which on that is so: half of the last-level cache, 256 MB.
+constexpr int64_t kPastCaches = 128 << 20;
+
 // ---------------------------------------------------------------------------
 // launchers
 // ---------------------------------------------------------------------------
