@@ -5,15 +5,20 @@
 
 namespace moe {
 
-// Blocks of the backward pass, each of which leaves one row of partial sums of
-// dgamma in the workspace: four per CU at most.
-constexpr int64_t kNormParts = 1024;
 // Rows that a block of 256 threads works on at once, by the width: 16, 64 or 256
 // lanes to a row.
 inline int norm_lanes(int64_t d) { return d <= 512 ? 16 : (d <= 2048 ? 64 : 256); }
+// Blocks of the backward pass, each of which leaves one row of partial sums of
+// dgamma in the workspace: four per CU at most, and, past one per CU, fewer than let each
+// walk over 16 rows (8 rows of more than 2048), since a row of sums in float32 is twice a
+// row of the input.  In us, dx and dgamma together, bf16, with a block for every row or four of
+// up to 2048 / with these: 1500 x 4096 26 / 16, 4096 x 4096 32 / 27, 2048 x 16384 99 / 52, 4096 x
+// 2048 19 / 16; 16 rows where it is 8: 1500 x 4096 17.  8192 x 640: 11.3 / 11.0, with 32 rows 13.6.
+constexpr int64_t kNormParts = 1024;
 inline int64_t norm_parts(int64_t T, int64_t d) {
-  const int64_t n = cdiv(T, 256 / norm_lanes(d));
-  return n < kNormParts ? n : kNormParts;
+  const int64_t at_once = 256 / norm_lanes(d), n = cdiv(T, at_once);
+  const int64_t m = T / (at_once == 1 ? 8 : 4 * at_once);
+  return n <= 256 ? n : (m < 256 ? 256 : (m < kNormParts ? m : kNormParts));
 }
 inline size_t norm_workspace_bytes(const moe_shape* s) {
   const size_t b = align_up((size_t)(norm_parts(s->T, s->d) * s->d) * sizeof(float), 256);

@@ -1,15 +1,16 @@
 // Root-mean-square norm of token rows, with the residual's addition before it and
 // the 8-bit rows behind it, and its backward pass (formulas in moe.h).
 // Both are one pass over memory, which bounds them: 65536 x 2048 bf16 forward with
-// residual, y and 8-bit rows 205 us (1.21 GB, 5.9 TB/s; 222 through the caches and with
-// 2048 blocks), backward with the residual's gradient 183 us (1.07 GB, 5.9 TB/s; 202).  A row is held in the registers
-// of 16, 64 or 256 lanes (d up to 512, 2048, 16384), eight consecutive elements of
-// a lane to a 16-byte load, so the sum of squares needs no second read, and 16
-// lanes hold a scale block of 128.  Sums are float32: a lane's own, then over the
-// lanes in a fixed order.
+// residual, y and 8-bit rows 203 us (1.21 GB, 6.0 TB/s; 222 through the caches and with
+// 2048 blocks), backward with the residual's gradient 183 us (1.07 GB, 5.9 TB/s; 202).  A
+// row is held in the registers of 16, 64 or 256 lanes (d up to 512, 2048, 16384), eight
+// consecutive elements of a lane to a 16-byte load, so the sum of squares needs no
+// second read, and 16 lanes hold a scale block of 128.  Sums are float32: a lane's own,
+// then over the lanes in a fixed order.
 // dgamma is a sum over all rows: a block keeps its columns' sums in registers while
 // it walks its rows, writes one row of them, and a second launch adds those rows in
-// a fixed order.
+// a fixed order.  For few rows dgamma's columns are summed by further blocks of the same
+// launch, which read dy and r again.
 #include "moe_fp8.h"
 #include "moe_norm.h"
 
@@ -17,6 +18,11 @@ namespace moe {
 namespace {
 
 constexpr int NT = 256;
+// Rows up to which dgamma is summed from a second reading of dy and r: in us, dx and
+// dgamma together in a graph, bf16, this way against partial sums: 333 x 640 3.8 / 5.4 (called one
+// by one 6.6 / 9.1), 700 x 2048 4.9 / 7.4, 1024 x 640 5.5 / 5.8, 1024 x 4096 11.7 / 14.4, 1024 x
+// 16384 43 / 38; 1500 x 640 6.7 / 6.3, 1500 x 2048 10.6 / 9.6, 2048 x 4096 25 / 19.
+constexpr int64_t kFewRows = 1024;
 
 // Eight consecutive elements as they lie in memory.
 template <typename T>
@@ -114,7 +120,8 @@ __global__ __launch_bounds__(NT) void rmsnorm_kernel(Fwd<T> a) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) f[i] += g[i];
         xr[c].pack(f);
-        if (a.r && on && c * L + lane < chunks) xr[c].template store<PAST>(a.r + at + (c * L + lane) * 8);
+        if (a.r && on && c * L + lane < chunks)
+          xr[c].template store<PAST>(a.r + at + (c * L + lane) * 8);
       }
     }
     auto squares = [&](float unit) {
@@ -183,14 +190,65 @@ struct Bwd {
   bool accumulate;  // with one block
   int64_t rows;
   int d;
+  float* dgamma;  // FEW: the blocks behind the first row_blocks sum its columns
+  int row_blocks;
 };
 
-template <typename T, int L, int C, bool PAST>
+// 32 columns of dgamma over all rows: four lanes to a row, 64 rows at a time, four in
+// flight; then the lanes of a wave and the waves.
+template <typename T>
+__device__ __forceinline__ void sum_columns(const Bwd<T>& a, int block) {
+  __shared__ float s[NT / 64][32];
+  const int part = threadIdx.x & 3, col = block * 32 + part * 8;
+  float acc[8] = {};
+  for (int64_t t0 = threadIdx.x >> 2; t0 < a.rows; t0 += 4 * (NT / 4)) {
+    Raw8<T> dy[4], r[4];
+    float rstd[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int64_t t = t0 + u * (NT / 4);
+      dy[u].zero();
+      r[u].zero();
+      rstd[u] = 0.f;
+      if (t < a.rows) {
+        dy[u].load(a.dy + t * a.d + col);
+        r[u].load(a.r + t * a.d + col);
+        rstd[u] = a.rstd[t];
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      float f[8], x[8];
+      dy[u].unpack(f);
+      r[u].unpack(x);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) acc[i] += f[i] * (x[i] * rstd[u]);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    float v = acc[i];
+#pragma unroll
+    for (int o = 4; o < 64; o <<= 1) v += __shfl_xor(v, o, 64);
+    if ((threadIdx.x & 63) < 4) s[threadIdx.x >> 6][part * 8 + i] = v;
+  }
+  __syncthreads();
+  const int j = threadIdx.x;
+  if (j < 32) {
+    const float v = (s[0][j] + s[1][j]) + (s[2][j] + s[3][j]);
+    float* p = a.dgamma + block * 32 + j;
+    *p = a.accumulate ? *p + v : v;
+  }
+}
+
+template <typename T, int L, int C, bool PAST, bool FEW>
 __global__ __launch_bounds__(NT) void rmsnorm_bwd_kernel(Bwd<T> a) {
+  if constexpr (FEW)
+    if ((int)blockIdx.x >= a.row_blocks) return sum_columns(a, (int)blockIdx.x - a.row_blocks);
   __shared__ float s_sum[2][NT / 64];
-  __shared__ float s_part[L == 256 ? 1 : NT / 64][L == 256 ? 1 : C * L * 8];
+  __shared__ float s_part[L == 256 || FEW ? 1 : NT / 64][L == 256 || FEW ? 1 : C * L * 8];
   const int lane = threadIdx.x & (L - 1), chunks = a.d >> 3;
-  const int64_t step = (int64_t)gridDim.x * (NT / L);
+  const int64_t step = (int64_t)(FEW ? a.row_blocks : gridDim.x) * (NT / L);
   const int64_t first = (int64_t)blockIdx.x * (NT / L);
   Raw8<T> gamma[C];
   float acc[C][8];
@@ -248,7 +306,7 @@ __global__ __launch_bounds__(NT) void rmsnorm_bwd_kernel(Bwd<T> a) {
       if (on && c * L + lane < chunks) o.template store<PAST>(a.dx + at + (c * L + lane) * 8);
     }
   }
-  if (!a.parts) return;  // block-uniform
+  if (FEW || !a.parts) return;  // block-uniform
   float* out = a.parts + (size_t)blockIdx.x * a.d;
   auto put = [&](float* p, float v) { *p = a.accumulate ? *p + v : v; };
   if constexpr (L == 256) {
@@ -334,15 +392,17 @@ template <typename T>
 struct GoBwd {
   Bwd<T> a;
   int grid;
-  bool past;
+  bool past, few;
   hipStream_t st;
   template <int L, int C>
   int operator()() const {
-    if (past)
-      MOE_LAUNCH("rmsnorm_bwd", st, rmsnorm_bwd_kernel<T, L, C, true><<<grid, NT, 0, st>>>(a));
-    else
-      MOE_LAUNCH("rmsnorm_bwd", st, rmsnorm_bwd_kernel<T, L, C, false><<<grid, NT, 0, st>>>(a));
-    return check_launch("rmsnorm_bwd");
+    auto go = [&](auto kernel) {
+      MOE_LAUNCH("rmsnorm_bwd", st, kernel<<<grid, NT, 0, st>>>(a));
+      return check_launch("rmsnorm_bwd");
+    };
+    if (few) return go(rmsnorm_bwd_kernel<T, L, C, false, true>);
+    return past ? go(rmsnorm_bwd_kernel<T, L, C, true, false>)
+                : go(rmsnorm_bwd_kernel<T, L, C, false, false>);
   }
 };
 
@@ -364,19 +424,24 @@ int rmsnorm_bwd_t(const moe_shape* s, const void* dy, const void* r, const void*
                   const float* rstd, const void* dres, void* dx, float* dgamma, bool accumulate,
                   float* parts, hipStream_t st) {
   const int n = (int)norm_parts(s->T, s->d);
+  const Bwd<T> a{(const T*)dy, (const T*)r, (const T*)gamma, rstd, (const T*)dres, (T*)dx, nullptr,
+                 accumulate, s->T, (int)s->d, dgamma, (int)cdiv(s->T, NT / norm_lanes(s->d))};
+  // the columns' blocks read dy and r beside blocks that write dx
+  if (dgamma && n > 1 && s->T <= kFewRows && dx != dy && dx != r)
+    return with_layout(s->d, GoBwd<T>{a, a.row_blocks + (int)(s->d / 32), false, true, st});
   if (n > 0) {
     const bool direct = n == 1;  // one block adds to dgamma itself
     float* p = !dgamma ? nullptr : (direct ? dgamma : parts);
-    if (int rc = with_layout(s->d, GoBwd<T>{{(const T*)dy, (const T*)r, (const T*)gamma, rstd,
-                                             (const T*)dres, (T*)dx, p, direct && accumulate,
-                                             s->T, (int)s->d}, n, past_caches<T>(s), st}))
-      return rc;
+    Bwd<T> b = a;
+    b.parts = p;
+    b.accumulate = direct && accumulate;
+    if (int rc = with_layout(s->d, GoBwd<T>{b, n, past_caches<T>(s), false, st})) return rc;
     if (!dgamma || direct) return MOE_OK;
   }
   if (!dgamma) return MOE_OK;
   MOE_LAUNCH("rmsnorm_dgamma", st,
-             rmsnorm_dgamma_kernel<<<(int)(s->d / 16), 1024, 0, st>>>(parts, n, (int)s->d, accumulate,
-                                                                    dgamma));
+             rmsnorm_dgamma_kernel<<<(int)(s->d / 16), 1024, 0, st>>>(parts, n, (int)s->d,
+                                                                      accumulate, dgamma));
   return check_launch("rmsnorm_dgamma");
 }
 

@@ -319,3 +319,22 @@ def test_long_batch():
     few.dy = o["y"]
     dx, _ = few.backward(few.x, o["rstd"], dres=False)
     assert torch.equal(dx, y[-7:]) and dg.isfinite().all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("T,d", [(1024, 640), (1025, 640), (1024, 2112), (1025, 2112), (17, 512),
+                                 (1024, 64), (4, 2048), (5, 2048), (2, 16384)])
+def test_dgamma_whichever_way_it_is_summed(T, d, dtype):
+    """Around the borders between the ways, and beside a dx that takes dy's or r's place,
+    where dy and r can be read once only."""
+    n = Norm(T, d, dtype, res=False, q=False)
+    o = n.forward()
+    dx, dg = n.backward(n.x, o["rstd"])
+    n.check_backward(n.x, o["rstd"], dx, dg)
+    dy, r = n.dy, n.x
+    for k in ("dy", "r"):
+        n.dy, at = dy.clone(), r.clone()
+        got, dg = n.backward(at, o["rstd"], dx=n.dy if k == "dy" else at)
+        n.dy = dy
+        assert torch.equal(got, dx), k
+        n.check_backward(r, o["rstd"], got, dg)
