@@ -2,11 +2,14 @@
 // (decoding, short prompts): one pass over the active experts' weights, so what bounds
 // them is how fast those stream from memory.  A block takes groups of 16 S weight rows (of
 // both halves for gate and up) of one expert; its four waves share the reduction by 256
-// values (128 bytes of a weight row), the weights go straight to registers and are the
-// M side of the MFMAs, up to 16 G token rows the N side.
+// values (128 bytes of a weight row; by 128 where there are 512 at most), the weights go
+// straight to registers and are the M side of the MFMAs, up to 16 G token rows the N side.
 // bf16 data: v_mfma_scale_f32_16x16x128_f8f6f4 on the codes as they are, with the scales
 // as bytes of the lanes.  fp16 data: codes and rows widened to bf16 with their scales
 // (exact) for 16 x 16 x 32 bf16 MFMAs.
+// 128 experts of 2048 x 768, bf16, both products: one token (8 experts, 20 MB) 12.4 us, two
+// launches of 6.7 and 5.0 whose chains of latencies (plan, weights, sum over waves) bound
+// them; 64 tokens (316 MB) 75 us, 4.2 TB/s of weights; 256 tokens 90.
 #include "moe_fp4.h"
 #include "moe_small8.h"
 
@@ -96,13 +99,13 @@ struct X32 {
   }
 };
 
-// A lane's codes of NW sets of 16 weight rows, values 32 (lane / 16) ..+31 of two blocks of
+// A lane's codes of NW sets of 16 weight rows, values 32 (lane / 16) ..+31 of UB blocks of
 // 128, and the scales of all four lanes of the row (byte lane / 16 of a word is its own): a
 // byte of each lane's own would be a request of its own, 20 % of the time.
-template <int S, int NW, bool PAIR>
+template <int S, int NW, int UB, bool PAIR>
 struct Weights {
-  i32x4_t v[NW][2];
-  uint32_t scale[NW][2];
+  i32x4_t v[NW][UB];
+  uint32_t scale[NW][UB];
   // q: the lane's codes, s: the row's scales, in block 0 of set 0.  Where the second block
   // does not exist the first's codes are read again, and nothing past the row's scales
   // (PAIR: one load for both blocks, where a row has two at least).
@@ -113,16 +116,20 @@ struct Weights {
     for (int w = 0; w < NW; ++w) {
       const size_t to = (size_t)(w / S * W.apart + w % S * 16);
       const uint8_t* p = q + to * (W.k / 2) + kb * 64;
-      v[w][0] = *(const i32x4_t*)p;
-      v[w][1] = *(const i32x4_t*)(p + (two ? 64 : 0));
       const uint8_t* b = s + to * (W.k / 32) + kb * 4;
+      v[w][0] = *(const i32x4_t*)p;
+      if constexpr (UB == 1) {
+        scale[w][0] = *(const uint32_t*)b;
+        continue;
+      }
+      v[w][UB - 1] = *(const i32x4_t*)(p + (two ? 64 : 0));
       if constexpr (PAIR) {
         const u32x2_t x = *(const u32x2_t*)(b - (two ? 0 : 4));
         scale[w][0] = two ? x[0] : x[1];
-        scale[w][1] = x[1];
+        scale[w][UB - 1] = x[1];
       } else {
         scale[w][0] = *(const uint32_t*)b;
-        scale[w][1] = *(const uint32_t*)(b + (two ? 4 : 0));
+        scale[w][UB - 1] = *(const uint32_t*)(b + (two ? 4 : 0));
       }
     }
   }
@@ -186,38 +193,94 @@ struct Second {
   }
 };
 
-// A block takes `span` groups of 16 S output columns of one expert, 16 G of its rows at a
-// time.  Its four waves take the units of the reduction (two blocks of 128) in turn, and
-// their sums meet in LDS for each group.  With UW units to a wave at most (0: any number) it
-// keeps its part of the rows in registers over the groups: read, and for the second product
-// quantised, once.  Each of BUF buffers is filled with the weights of the unit that will use it
-// next as soon as its last ones are used: no weights are moved between registers, which
-// would wait for them.
-template <int S, int G, int UW, class Op>
+// Sum over the lanes up to this one.
+__device__ __forceinline__ int sum_to_lane(int v) {
+  auto add = [&](int x) { v += x; };
+  add(__builtin_amdgcn_update_dpp(0, v, 0x111, 0xF, 0xF, true));   // within rows of 16: from 1,
+  add(__builtin_amdgcn_update_dpp(0, v, 0x112, 0xF, 0xF, true));   // 2,
+  add(__builtin_amdgcn_update_dpp(0, v, 0x114, 0xF, 0xF, true));   // 4
+  add(__builtin_amdgcn_update_dpp(0, v, 0x118, 0xF, 0xF, true));   // and 8 lanes below
+  add(__builtin_amdgcn_update_dpp(0, v, 0x142, 0xA, 0xF, false));  // lane 15 and 47 to the next row
+  add(__builtin_amdgcn_update_dpp(0, v, 0x143, 0xC, 0xF, false));  // lane 31 to the upper half
+  return v;
+}
+
+// Pass number `slot` over at most ROWS rows of one expert, the experts in order; false if
+// there are fewer.  Every wave finds it by itself.
+template <int ROWS>
+__device__ __forceinline__ bool nth_pass(const int32_t* offsets, int E_l, int slot, int& e,
+                                         int& r0, int& m_end) {
+  const int lane = (int)(threadIdx.x & 63);
+  int lo[4], hi[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const int j = min(k * 64 + lane, E_l - 1);
+    lo[k] = offsets[j];
+    hi[k] = k * 64 + lane < E_l ? offsets[j + 1] : lo[k];
+  }
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    if (k * 64 >= E_l) break;  // uniform
+    const int n = (hi[k] - lo[k] + ROWS - 1) / ROWS;
+    const uint64_t some = __ballot(n > 0), many = __ballot(n > 1);
+    int upto, total;  // passes up to this lane's expert, and of all 64
+    if (many == 0) {  // wave-uniform: most often, and the shorter way
+      upto = (int)__builtin_amdgcn_mbcnt_hi((uint32_t)(some >> 32),
+                                            __builtin_amdgcn_mbcnt_lo((uint32_t)some, 0u)) + n;
+      total = (int)__popcll(some);
+    } else {
+      upto = sum_to_lane(n);
+      total = __builtin_amdgcn_readlane(upto, 63);
+    }
+    if (slot < total) {  // wave-uniform
+      const int l = __builtin_ctzll(__ballot(slot < upto));
+      const int before = __builtin_amdgcn_readlane(upto, l) - __builtin_amdgcn_readlane(n, l);
+      e = k * 64 + l;
+      r0 = __builtin_amdgcn_readlane(lo[k], l) + (slot - before) * ROWS;
+      m_end = __builtin_amdgcn_readlane(hi[k], l);
+      return true;
+    }
+    slot -= total;
+  }
+  return false;
+}
+
+// A block takes `span` groups of 16 S output columns for a pass, 16 G rows of one expert.  Its
+// four waves take the units of the reduction (UB blocks of 128) in turn, and their sums meet
+// in LDS for each group.  With UW units to a wave at most (0: any number) it keeps its part of
+// the rows in registers over the groups: read, and for the second product quantised, once.
+// Each of BUF buffers is filled with the weights of the unit that will use it next as soon as
+// its last ones are used: no weights are moved between registers, which would wait for them.
+template <int S, int G, int UW, int UB, class Op>
 __global__ __launch_bounds__(64 * WAVES) void fp4_small_kernel(
-    Op op, WRows4 W, const int32_t* __restrict__ offsets, int E_l, int groups, int span) {
+    Op op, WRows4 W, const int32_t* __restrict__ offsets, int E_l, int groups, int span,
+    int most) {
   constexpr int NW = Op::H * S, HELD = UW > 0 ? UW : 1, BUF = 2;
   constexpr bool WIDE = Op::WIDE;
   __shared__ Reduce<NW, G> red;
-  int e, m0, m_end;
-  if (!nth_expert(offsets, E_l, blockIdx.y, e, m0, m_end)) return;  // block-uniform
   const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
   const int lane = threadIdx.x & 63, part = lane >> 4;
   const int c_first = blockIdx.x * span, c_end = min(c_first + span, groups);
-  const int kbs = W.k / 128, units = (kbs + 1) / 2;
+  const int kbs = W.k / 128, units = (kbs + UB - 1) / UB;
   const int n = (units - wave + WAVES - 1) / WAVES;  // of this wave
-  const size_t row0 = (size_t)e * W.n + (lane & 15);
-  const uint8_t* q = W.q + row0 * (W.k / 2) + part * 16;
-  const uint8_t* s = W.s + row0 * (W.k / 32);
-  auto block = [&](int i) { return (wave + i * WAVES) * 2; };  // the first of unit i
-  Weights<S, NW, (UW > 0)> buf[BUF];
-  // unit i of group c, if there is such a group
-  auto fetch = [&](auto& w, int c, int i) {
-    if (c < c_end)  // block-uniform
-      w.load(W, q + (size_t)(c * 16 * S) * (W.k / 2), s + (size_t)(c * 16 * S) * (W.k / 32),
-             block(i));
-  };
-  for (int r0 = m0 + blockIdx.z * 16 * G; r0 < m_end; r0 += gridDim.z * 16 * G) {
+  auto block = [&](int i) { return (wave + i * WAVES) * UB; };  // the first of unit i
+  int e, r0, m_end;
+  // No load has more than `most` passes.  Where passes are of 32 rows or more the grid has
+  // them all: the loop would cost 30 registers and a wave per SIMD (23.6 us instead of 27.4, 8 of
+  // 64 experts of 2048 x 1408 at 19 rows; with passes of 16 rows, whose weights bound them, it
+  // is 4 % faster with the loop).
+  for (int slot = blockIdx.y; slot < most && nth_pass<16 * G>(offsets, E_l, slot, e, r0, m_end);
+       slot += gridDim.y) {  // block-uniform
+    const size_t row0 = (size_t)e * W.n + (lane & 15);
+    const uint8_t* q = W.q + row0 * (W.k / 2) + part * 16;
+    const uint8_t* s = W.s + row0 * (W.k / 32);
+    Weights<S, NW, UB, (UW > 0)> buf[BUF];
+    // unit i of group c, if there is such a group
+    auto fetch = [&](auto& w, int c, int i) {
+      if (c < c_end)  // block-uniform
+        w.load(W, q + (size_t)(c * 16 * S) * (W.k / 2), s + (size_t)(c * 16 * S) * (W.k / 32),
+               block(i));
+    };
     // the rows' places are asked for ahead of the weights, behind which their loads, in
     // order, would wait
     int at[G];
@@ -233,10 +296,10 @@ __global__ __launch_bounds__(64 * WAVES) void fp4_small_kernel(
     typename Op::template X<G> x;
 #pragma unroll
     for (int g = 0; g < G; ++g) op.rows(x, g, at[g]);
-    Tokens<WIDE> held[HELD][2][G];
-    auto hold = [&](Tokens<WIDE> (&to)[2][G], int kb) {
+    Tokens<WIDE> held[HELD][UB][G];
+    auto hold = [&](Tokens<WIDE> (&to)[UB][G], int kb) {
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
+      for (int h = 0; h < UB; ++h)
 #pragma unroll
         for (int g = 0; g < G; ++g) to[h][g] = x.get(min(kb + h, kbs - 1), g, part);
     };
@@ -263,9 +326,9 @@ __global__ __launch_bounds__(64 * WAVES) void fp4_small_kernel(
       __syncthreads();
     };
     f32x4_t acc[NW][G];
-    auto unit = [&](auto& w, int i, const Tokens<WIDE> (&b)[2][G]) {
+    auto unit = [&](auto& w, int i, const Tokens<WIDE> (&b)[UB][G]) {
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
+      for (int h = 0; h < UB; ++h) {
         if (h == 1 && block(i) + 1 >= kbs) break;  // wave-uniform
 #pragma unroll
         for (int v = 0; v < NW; ++v)
@@ -322,27 +385,39 @@ __global__ __launch_bounds__(64 * WAVES) void fp4_small_kernel(
         finish_group(c, acc);
       }
     }
+    if constexpr (G > 1) break;
   }
 }
 
-// Blocks that share the groups where the routing is even: two per CU.
-constexpr int kBlocks = 512;
+// Blocks that share the groups where the routing is even: two per CU; and in all, those that
+// only a skewed load needs, which leave at once in others.
+constexpr int kBlocks = 512, kMostBlocks = 4096;
 
 template <class Op>
 int launch(const char* name, const moe_shape* s, const Op& op, const WRows4& W, int cols,
            const int32_t* offsets, hipStream_t st) {
   const Shape sh(s, cols, Op::H == 1);
   const int groups = (int)sh.grid.x;
-  // experts that have rows
-  const double with_rows =
-      std::max(1.0, (double)s->E_l * -expm1(-(double)(s->T * s->K) / (double)s->E));
-  const int parts = (int)std::max(1.0, kBlocks / (with_rows * sh.grid.z) + 0.5);
-  const int span = (int)cdiv(groups, std::min(parts, groups));
-  const dim3 grid((unsigned)cdiv(groups, span), sh.grid.y, sh.grid.z);
-  const int units = (W.k + 255) / 256, per_wave = (units + WAVES - 1) / WAVES;
+  // passes of an even load: experts that have rows, times the passes over what most have at
+  // most (as in Shape; with the mean alone 25 us instead of 23, 8 experts of 2048 x 768, 32 rows)
+  const int64_t pairs = s->T * s->K, rows = 16 * sh.G;
+  const double mean = (double)pairs / (double)s->E;
+  const double passes =
+      std::max(1.0, s->E_l * -expm1(-mean)) * ceil((mean + 2 * sqrt(mean)) / (double)rows);
+  // and of any load
+  const int64_t slots = std::max<int64_t>(1, std::min(pairs, s->E_l));
+  const int64_t most = std::min(slots + pairs / rows, slots * cdiv(s->T, rows));
+  const int64_t parts = std::min<int64_t>(
+      {(int64_t)(kBlocks / passes + 0.5), groups, sh.G == 1 ? groups : kMostBlocks / most});
+  const int span = (int)cdiv(groups, std::max<int64_t>(1, parts));
+  const int64_t x = cdiv(groups, span);
+  const int64_t y =
+      sh.G == 1 ? std::min(most, std::max(2 * (int64_t)ceil(passes), cdiv(1024, x))) : most;
+  const dim3 grid((unsigned)x, (unsigned)y);
+  const int per_wave = (W.k + 256 * WAVES - 1) / (256 * WAVES);
   auto go = [&](auto kernel) {
     MOE_LAUNCH(name, st, kernel<<<grid, 64 * WAVES, 0, st>>>(op, W, offsets, (int)s->E_l, groups,
-                                                             span));
+                                                             span, (int)most));
     return check_launch(name);
   };
   auto by_rows = [&](auto S_) {
@@ -350,10 +425,12 @@ int launch(const char* name, const moe_shape* s, const Op& op, const WRows4& W, 
     // as many units' rows in registers as leave two waves to a SIMD
     auto by_units = [&](auto G_, auto most) {
       constexpr int G = decltype(G_)::value, MOST = decltype(most)::value;
-      if (per_wave > MOST || W.k == 128) return go(fp4_small_kernel<S, G, 0, Op>);
+      // one block of 128 to a wave where that is all
+      if (W.k <= 128 * WAVES) return go(fp4_small_kernel<S, G, 1, 1, Op>);
+      if (per_wave > MOST) return go(fp4_small_kernel<S, G, 0, 2, Op>);
       if constexpr (MOST == 2)
-        if (per_wave == 2) return go(fp4_small_kernel<S, G, 2, Op>);
-      return go(fp4_small_kernel<S, G, 1, Op>);
+        if (per_wave == 2) return go(fp4_small_kernel<S, G, 2, 2, Op>);
+      return go(fp4_small_kernel<S, G, 1, 2, Op>);
     };
     typedef std::integral_constant<int, 1> One;
     typedef std::integral_constant<int, 2> Two;
@@ -388,22 +465,25 @@ int ffn_fwd_t(const moe_shape* s, const void* xq, const uint8_t* xs, const int32
 // 5e7 in bf16 and 7e7 in fp16, 256 at most.  Below it these kernels are faster than the tiles,
 // whose time hardly falls with the rows; above, more than 32 rows of an expert take a pass
 // over its weights each, or more registers than leave two waves to a SIMD.  Both sides in us
-// on an MI355X, forward, small against tiles: bf16, 128 experts of 2048 x 768 at 8 rows 88 / 121,
-// at 16 96 / 121, at 20 124 / 122, at 24 146 / 123; 64 of them at 20 62 / 76, at 24 84 / 75; 16 of
-// 4096 x 1024 at 20 53 / 60, at 25 68 / 60; 8 of 2048 x 1408 at 21 25 / 37, at 26 50 / 37; 8 of
-// 2048 x 768 at 32 23 / 32, at 64 29 / 33; 4 of 640 x 384 at 256 15 / 26, at 400 29 / 23.  fp16: 128
-// of 2048 x 768 at 16 136 / 151, at 20 183 / 152; 8 of 2048 x 1408 at 21 39 / 54, at 26 58 / 55; 8 of
-// 2048 x 768 at 64 40 / 49, at 128 67 / 50.
-// As for the 8-bit kernels, no block may need more than 8 passes with every token on one
-// expert.
+// on an MI355X, forward, small against tiles: bf16, 128 experts of 2048 x 768 at 8 rows 83 / 117,
+// at 16 90 / 117, at 20 123 / 118, at 24 143 / 119; 64 of them at 20 51 / 74, at 24 83 / 75; 16 of
+// 4096 x 1024 at 20 50 / 59, at 25 67 / 60; 8 of 2048 x 1408 at 21 24 / 37, at 26 39 / 37; 8 of
+// 2048 x 768 at 32 24 / 32, at 64 37 / 33; 8 of 1024 x 256 at 184 19 / 24; 4 of 640 x 384 at 256
+// 15 / 25.  fp16: 128 of 2048 x 768 at 16 125 / 150, at 20 165 / 150; 8 of 2048 x 1408 at 21
+// 34 / 55; 8 of 2048 x 768 at 64 47 / 49, at 128 66 / 50.
+// These are even loads.  A fuller expert takes more passes, each over its weights again from
+// L2: 128 experts of 2048 x 768, Zipf 1.1, at 4 rows 62 / 74, at 16 88 / 99; 8 of 64 of 2048 x
+// 1408 at 19 65 / 40; one of 512 of 2048 x 768 at 16 (the fullest, 950 rows) 85 / 34 where its
+// even load is 10 / 30.  So that it stays within a few times the tiles' time, no expert may
+// take more than 64 passes with every token.
 static int64_t most_mean(const moe_shape* s) {
   const bool bf16 = s->dtype == MOE_BF16;
   const double more = (bf16 ? 5e7 : 7e7) / ((double)s->E_l * (double)s->F * (double)s->d);
   return std::min<int64_t>(256, (bf16 ? 20 : 17) + (int64_t)std::min(256.0, more * more));
 }
 bool fp4_small(const moe_shape* s) {
-  return cdiv(s->T * s->K, s->E) <= most_mean(s) &&
-         std::max(Shape(s, (int)s->F, false).passes, Shape(s, (int)s->d, true).passes) <= 8;
+  const int64_t rows = 16 * std::min(Shape(s, (int)s->F, false).G, Shape(s, (int)s->d, true).G);
+  return cdiv(s->T * s->K, s->E) <= most_mean(s) && cdiv(s->T, rows) <= 64;
 }
 // For the longest batch of at most T tokens that these kernels take.
 size_t fp4_small_workspace_bytes(const moe_shape* s) {

@@ -285,3 +285,48 @@ def test_other_shape_is_refused():
     s = M.make_shape(16, 256, 128, 8, 0, 8, 8, "bf16")
     with pytest.raises(M.MoeError):
         M.moe_quant_weights_fp4(s, L.W_gu, L.W_down, L.w4)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("T,d,F,E,E_l,K,on", [
+    (100, 256, 128, 64, 16, 1, [0]), (257, 256, 128, 4, 4, 1, [2]),
+    (700, 128, 128, 128, 16, 1, [9]),
+    (1000, 1024, 256, 8, 8, 1, [5]), (150, 128, 256, 64, 16, 8, list(range(8))),
+    (600, 256, 2048, 512, 1, 8, [0]),       # more passes than the grid holds at once
+    (600, 128, 2048, 512, 3, 8, [1, 2, 7, 8, 9, 10, 11, 12]),
+    (333, 640, 384, 256, 256, 8, [3, 64, 65, 127, 128, 191, 192, 255]),
+])
+def test_all_tokens_on_the_same_experts(T, d, F, E, E_l, K, on, dtype):
+    L = Layer4(T, d, F, E, 0, E_l, K, dtype, True, only=on)
+    assert max(L.off[1:] - L.off[:-1]) == T
+    L.check_forward(L.forward())
+
+
+@pytest.mark.parametrize("T,d,F,E,E_l,K,small", [
+    (129, 512, 256, 128, 128, 7, True),      # 7 rows each on average, up to 129
+    (4096, 256, 128, 64, 8, 1, False),       # 64 on average, in passes of 16, up to 4096
+    (1100, 256, 128, 512, 1, 4, False),      # 9 rows on average, up to 1100
+    (16384, 256, 128, 512, 1, 8, False),
+])
+def test_which_kernels_run(T, d, F, E, E_l, K, small):
+    L = Layer4(T, d, F, E, 0, E_l, K, "bf16", True)
+    M.moe_timing_enable()
+    try:
+        M.moe_timing_reset()
+        out = L.forward()
+        torch.cuda.synchronize()
+        names = set(M.moe_timing_report())
+    finally:
+        M.moe_timing_disable()
+    assert len(names) == 2 and all(n.endswith("_small") == small for n in names), names
+    L.check_forward(out)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("d,F", [(128, 128), (384, 256), (512, 512), (640, 384), (1024, 1152),
+                                 (2176, 128), (256, 2432)])
+def test_every_length_of_the_reduction(d, F, dtype):
+    """One block to a wave, two, two units of two, and more; the last one half."""
+    for T, E, K in ((3, 4, 2), (50, 4, 2), (150, 4, 1)):
+        L = Layer4(T, d, F, E, 0, E, K, dtype, True, seed=d)
+        L.check_forward(L.forward())
