@@ -7,8 +7,8 @@
 // bf16 data: v_mfma_scale_f32_16x16x128_f8f6f4 on the codes as they are, with the scales
 // as bytes of the lanes.  fp16 data: codes and rows widened to bf16 with their scales
 // (exact) for 16 x 16 x 32 bf16 MFMAs.
-// 128 experts of 2048 x 768, bf16, both products: one token (8 experts, 20 MB) 12.4 us, two
-// launches of 6.7 and 5.0 whose chains of latencies (plan, weights, sum over waves) bound
+// 128 experts of 2048 x 768, bf16, both products: one token (8 experts, 20 MB) 11.8 us, two
+// launches of 6.5 and 5.0 whose chains of latencies (plan, weights, sum over waves) bound
 // them; 64 tokens (316 MB) 75 us, 4.2 TB/s of weights; 256 tokens 90.
 #include "moe_fp4.h"
 #include "moe_small8.h"
@@ -216,12 +216,12 @@ __device__ __forceinline__ bool nth_pass(const int32_t* offsets, int E_l, int sl
   for (int k = 0; k < 4; ++k) {
     const int j = min(k * 64 + lane, E_l - 1);
     lo[k] = offsets[j];
-    hi[k] = k * 64 + lane < E_l ? offsets[j + 1] : lo[k];
+    hi[k] = offsets[j + 1];
   }
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
     if (k * 64 >= E_l) break;  // uniform
-    const int n = (hi[k] - lo[k] + ROWS - 1) / ROWS;
+    const int n = k * 64 + lane < E_l ? (hi[k] - lo[k] + ROWS - 1) / ROWS : 0;
     const uint64_t some = __ballot(n > 0), many = __ballot(n > 1);
     int upto, total;  // passes up to this lane's expert, and of all 64
     if (many == 0) {  // wave-uniform: most often, and the shorter way
@@ -251,7 +251,7 @@ __device__ __forceinline__ bool nth_pass(const int32_t* offsets, int E_l, int sl
 // the rows in registers over the groups: read, and for the second product quantised, once.
 // Each of BUF buffers is filled with the weights of the unit that will use it next as soon as
 // its last ones are used: no weights are moved between registers, which would wait for them.
-template <int S, int G, int UW, int UB, class Op>
+template <int S, int G, int UW, int UB, bool LOOP, class Op>
 __global__ __launch_bounds__(64 * WAVES) void fp4_small_kernel(
     Op op, WRows4 W, const int32_t* __restrict__ offsets, int E_l, int groups, int span,
     int most) {
@@ -265,10 +265,7 @@ __global__ __launch_bounds__(64 * WAVES) void fp4_small_kernel(
   const int n = (units - wave + WAVES - 1) / WAVES;  // of this wave
   auto block = [&](int i) { return (wave + i * WAVES) * UB; };  // the first of unit i
   int e, r0, m_end;
-  // No load has more than `most` passes.  Where passes are of 32 rows or more the grid has
-  // them all: the loop would cost 30 registers and a wave per SIMD (23.6 us instead of 27.4, 8 of
-  // 64 experts of 2048 x 1408 at 19 rows; with passes of 16 rows, whose weights bound them, it
-  // is 4 % faster with the loop).
+  // no load has more than `most` passes; without LOOP the grid has them all
   for (int slot = blockIdx.y; slot < most && nth_pass<16 * G>(offsets, E_l, slot, e, r0, m_end);
        slot += gridDim.y) {  // block-uniform
     const size_t row0 = (size_t)e * W.n + (lane & 15);
@@ -385,7 +382,7 @@ __global__ __launch_bounds__(64 * WAVES) void fp4_small_kernel(
         finish_group(c, acc);
       }
     }
-    if constexpr (G > 1) break;
+    if constexpr (!LOOP) break;
   }
 }
 
@@ -407,12 +404,18 @@ int launch(const char* name, const moe_shape* s, const Op& op, const WRows4& W, 
   // and of any load
   const int64_t slots = std::max<int64_t>(1, std::min(pairs, s->E_l));
   const int64_t most = std::min(slots + pairs / rows, slots * cdiv(s->T, rows));
+  // A grid of fewer passes, whose blocks take further ones, where the pass is of 16 rows and
+  // there may be more than 24.  The loop costs 30 registers and a wave per SIMD, in us with /
+  // without: one token, 128 experts of 2048 x 768 12.0 / 11.8, 100 of 8 of 64 experts of 2048 x
+  // 1408 19.5 / 18.9, 200 of them (32 rows) 27.4 / 23.6; but the weights of many experts stream
+  // better with it: 64 tokens, 128 experts 75 / 79, 8 of them 40 / 42.
+  const bool loop = sh.G == 1 && most > 24;
   const int64_t parts = std::min<int64_t>(
-      {(int64_t)(kBlocks / passes + 0.5), groups, sh.G == 1 ? groups : kMostBlocks / most});
+      {(int64_t)(kBlocks / passes + 0.5), groups, loop ? groups : kMostBlocks / most});
   const int span = (int)cdiv(groups, std::max<int64_t>(1, parts));
   const int64_t x = cdiv(groups, span);
   const int64_t y =
-      sh.G == 1 ? std::min(most, std::max(2 * (int64_t)ceil(passes), cdiv(1024, x))) : most;
+      loop ? std::min(most, std::max(2 * (int64_t)ceil(passes), cdiv(1024, x))) : most;
   const dim3 grid((unsigned)x, (unsigned)y);
   const int per_wave = (W.k + 256 * WAVES - 1) / (256 * WAVES);
   auto go = [&](auto kernel) {
@@ -423,22 +426,25 @@ int launch(const char* name, const moe_shape* s, const Op& op, const WRows4& W, 
   auto by_rows = [&](auto S_) {
     constexpr int S = decltype(S_)::value;
     // as many units' rows in registers as leave two waves to a SIMD
-    auto by_units = [&](auto G_, auto most) {
-      constexpr int G = decltype(G_)::value, MOST = decltype(most)::value;
+    auto by_units = [&](auto G_, auto most_, auto loop_) {
+      constexpr int G = decltype(G_)::value, MOST = decltype(most_)::value;
+      constexpr bool LOOP = decltype(loop_)::value;
       // one block of 128 to a wave where that is all
-      if (W.k <= 128 * WAVES) return go(fp4_small_kernel<S, G, 1, 1, Op>);
-      if (per_wave > MOST) return go(fp4_small_kernel<S, G, 0, 2, Op>);
+      if (W.k <= 128 * WAVES) return go(fp4_small_kernel<S, G, 1, 1, LOOP, Op>);
+      if (per_wave > MOST) return go(fp4_small_kernel<S, G, 0, 2, LOOP, Op>);
       if constexpr (MOST == 2)
-        if (per_wave == 2) return go(fp4_small_kernel<S, G, 2, 2, Op>);
-      return go(fp4_small_kernel<S, G, 1, 2, Op>);
+        if (per_wave == 2) return go(fp4_small_kernel<S, G, 2, 2, LOOP, Op>);
+      return go(fp4_small_kernel<S, G, 1, 2, LOOP, Op>);
     };
     typedef std::integral_constant<int, 1> One;
     typedef std::integral_constant<int, 2> Two;
     if (sh.G == 4)
       return by_units(std::integral_constant<int, 4>{},
-                      std::integral_constant<int, Op::WIDE || S == 4 ? 1 : 2>{});
-    if (sh.G == 2) return by_units(Two{}, std::integral_constant<int, Op::WIDE ? 1 : 2>{});
-    return by_units(One{}, Two{});
+                      std::integral_constant<int, Op::WIDE || S == 4 ? 1 : 2>{}, std::false_type{});
+    if (sh.G == 2)
+      return by_units(Two{}, std::integral_constant<int, Op::WIDE ? 1 : 2>{}, std::false_type{});
+    if (loop) return by_units(One{}, Two{}, std::true_type{});
+    return by_units(One{}, Two{}, std::false_type{});
   };
   if constexpr (Op::H == 1)
     if (sh.S == 4) return by_rows(std::integral_constant<int, 4>{});

@@ -2,7 +2,7 @@
 // blocks and neither codes nor scales are padded, so a matrix is one flat list of
 // blocks of 32: a thread holds eight consecutive values (16 bytes in 16 bits, a
 // register of codes), four threads a block.  Bound by memory: 128 experts of 2048 x 768
-// bf16 (1.53 GB) quantised in 242 us (6.3 TB/s), read back in 251 (6.1); 267 and 272 with four
+// bf16 (1.53 GB) quantised in 239 us (6.4 TB/s), read back in 252 (6.1); 267 and 272 with four
 // groups to a thread and through the caches.
 #include "moe_fp4.h"
 

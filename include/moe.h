@@ -709,8 +709,13 @@ size_t moe_fp4_workspace_bytes(const moe_shape* s);
 /*
  * moe_expert_ffn_fwd_fp4 - moe_expert_ffn_fwd_fp8 with the weights in 4 bits: 8-bit rows
  * (moe_quant_rows_fp8, moe_rmsnorm) on 4-bit weights, a quantised to 8 bits between
- * the two products.  Arguments, sums and rows >= N as there; w as above.  With T = 0
+ * the two products.  Arguments and rows >= N as there; w as above.  With T = 0
  * nothing is done and the other pointers may be NULL.
+ *   Sums.  MOE_F16: products and scales are exact and are summed in float32.  MOE_BF16:
+ * the scaled matrix instruction, which cuts products as described for the 8-bit calls,
+ * for few rows per expert too.  Equal calls give equal bits; with few rows per expert a
+ * row's results depend on its own operands and the shape alone, with more the last
+ * bits of yp may differ beside other rows, as there.
  *   ws: moe_fp4_workspace_bytes.
  */
 int moe_expert_ffn_fwd_fp4(const moe_shape* s, const void* xq, const uint8_t* xs,
