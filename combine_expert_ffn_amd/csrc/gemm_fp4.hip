@@ -18,11 +18,11 @@
 // In variants with parts left out: fragment reads and MFMAs alone 292 / 184, with the copies
 // 339 / 193, the epilogues without their stores 66 / 36 more, the stores (past the caches;
 // through them 31 more in all) 50 / 35.  The matrix cores are busy 45 and 38 % of it.
-// fp16: 5740 rows on 8 experts of 2048 x 1408 85 and 38 us (0.78 and 0.88 PFLOP/s), 1.1 rounds of
-// tiles on 256 CUs.
+// fp16: 1333 tokens, 8 of 64 experts of 2048 x 1408, K = 6, Zipf 85 and 38 us: little more than one
+// round of tiles on 256 CUs.
 // Slower: two blocks of 128 x 256 per CU (781 us for both products; 5 to 10 % faster at a few
-// hundred rows per expert), a ring of four stages with tiles of 128 rows (372 us for 512 rows
-// each as against 534, and no faster below), the first slice without clearing (350 registers
+// hundred rows per expert), a ring of four stages with tiles of 128 rows (534 us for 512 rows
+// each instead of 372, and no faster below), the first slice without clearing (350 registers
 // in memory).
 #include "moe_fp4.h"
 #include "moe_tile8.h"
