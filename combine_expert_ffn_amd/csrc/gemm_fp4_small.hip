@@ -401,9 +401,9 @@ int launch(const char* name, const moe_shape* s, const Op& op, const WRows4& W, 
   const double mean = (double)pairs / (double)s->E;
   const double passes =
       std::max(1.0, s->E_l * -expm1(-mean)) * ceil((mean + 2 * sqrt(mean)) / (double)rows);
-  // and of any load
+  // and of any load, tokens that name an expert more than once among them
   const int64_t slots = std::max<int64_t>(1, std::min(pairs, s->E_l));
-  const int64_t most = std::min(slots + pairs / rows, slots * cdiv(s->T, rows));
+  const int64_t most = slots + pairs / rows;
   // A grid of fewer passes, whose blocks take further ones, where the pass is of 16 rows and
   // there may be more than 24.  The loop costs 30 registers and a wave per SIMD, in us with /
   // without: one token, 128 experts of 2048 x 768 12.0 / 11.8, 100 of 8 of 64 experts of 2048 x
@@ -481,7 +481,7 @@ int ffn_fwd_t(const moe_shape* s, const void* xq, const uint8_t* xs, const int32
 // L2: 128 experts of 2048 x 768, Zipf 1.1, at 4 rows 62 / 74, at 16 88 / 99; 8 of 64 of 2048 x
 // 1408 at 19 65 / 40; one of 512 of 2048 x 768 at 16 (the fullest, 950 rows) 85 / 34 where its
 // even load is 10 / 30.  So that it stays within a few times the tiles' time, no expert may
-// take more than 64 passes with every token.
+// take more than 64 passes with every token once.
 static int64_t most_mean(const moe_shape* s) {
   const bool bf16 = s->dtype == MOE_BF16;
   const double more = (bf16 ? 5e7 : 7e7) / ((double)s->E_l * (double)s->F * (double)s->d);

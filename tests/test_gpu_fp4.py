@@ -330,3 +330,19 @@ def test_every_length_of_the_reduction(d, F, dtype):
     for T, E, K in ((3, 4, 2), (50, 4, 2), (150, 4, 1)):
         L = Layer4(T, d, F, E, 0, E, K, dtype, True, seed=d)
         L.check_forward(L.forward())
+
+
+@pytest.mark.parametrize("T,d,F,E,K", [
+    (1, 256, 128, 8, 8), (3, 128, 256, 64, 8), (16, 256, 128, 16, 4), (40, 640, 384, 8, 6),
+    (150, 128, 128, 16, 8), (700, 128, 128, 4, 4)])
+def test_tokens_that_name_an_expert_more_than_once(T, d, F, E, K):
+    """An expert then has up to K T rows."""
+    L = Layer4(T, d, F, E, 0, E, K, "bf16", True)
+    L.mb.idx.copy_(torch.where(torch.arange(K) == K - 1, E - 1, 0).to(torch.int32).expand(T, K))
+    ws = torch.empty(M.moe_workspace_bytes(L.s), dtype=torch.uint8, device="cuda")
+    M.moe_dispatch(L.s, None, L.mb.idx, L.mb.counts, L.mb.offsets, L.mb.row_of_pair,
+                   L.mb.pair_of_row, L.mb.tile_offsets, None, ws)
+    L.off = host(L.mb.offsets)
+    L.N, L.pair = int(L.off[-1]), host(L.mb.pair_of_row)[: int(L.off[-1])]
+    assert L.N == T * K and L.off[1] == T * (K - 1)
+    L.check_forward(L.forward())
