@@ -713,7 +713,10 @@ size_t moe_fp4_workspace_bytes(const moe_shape* s);
  * nothing is done and the other pointers may be NULL.
  *   Sums.  MOE_F16: products and scales are exact and are summed in float32.  MOE_BF16:
  * the scaled matrix instruction, which cuts products as described for the 8-bit calls,
- * for few rows per expert too.  Equal calls give equal bits; with few rows per expert a
+ * for few rows per expert too (where the 8-bit calls are exact).  h and a keep the error of
+ * their rounding; a value of a next to the border between two e4m3 values may be quantised
+ * to either.  A caller who needs exact products takes MOE_F16, or moe_expert_ffn_fwd on the
+ * weights read back.  Equal calls give equal bits; with few rows per expert a
  * row's results depend on its own operands and the shape alone, with more the last
  * bits of yp may differ beside other rows, as there.
  *   ws: moe_fp4_workspace_bytes.
