@@ -135,15 +135,15 @@ __global__ __launch_bounds__(NT) void rmsnorm_kernel(Fwd<T> a) {
       }
       return sum;
     };
-    // Where the sum passes float32's range (values of 1e17 and more) the row is taken in
-    // units of 2^80; eps is nothing beside it then.
-    float unit = 1.f, sum = row_sum<L>(squares(1.f), s_sum, turn);
-    if (sum == __builtin_inff()) {  // the same for all lanes of the row
+    // Where the sum, or the mean with eps, passes float32's range (values of 1e17 and more)
+    // the row is taken in units of 2^80, eps with it (in two steps: 2^-160 is no float32).
+    float unit = 1.f, mean = row_sum<L>(squares(1.f), s_sum, turn) / (float)a.d + a.eps;
+    if (mean == __builtin_inff()) {  // the same for all lanes of the row
       unit = 0x1p-80f;
       if constexpr (L == 256) ++turn;
-      sum = row_sum<L>(squares(unit), s_sum, turn);
+      mean = row_sum<L>(squares(unit), s_sum, turn) / (float)a.d + a.eps * unit * unit;
     }
-    const float root = 1.0f / sqrtf(sum / (float)a.d + (unit == 1.f ? a.eps : 0.f));
+    const float root = 1.0f / sqrtf(mean);
     const float rstd = root * unit;
     if (a.rstd && on && lane == 0) a.rstd[row] = rstd;
 #pragma unroll

@@ -631,9 +631,9 @@ int moe_ffn_dgrad_fp8(const moe_shape* s, const void* dq, const uint8_t* ds,
  *   y [T,d] out (dtype) or NULL; q [T,d] e4m3 and qs [T,ld(d)] out, or both NULL;
  *   at least one of y and q (MOE_ERR_NULL)
  *   rstd [T] f32 out or NULL: what the backward needs
- * Sums are float32 (rows with values past 1e17 are summed in units of 2^80, so none
- * overflows).  A value that is not finite reaches its own row alone (NaN: all of it; an
- * infinity: NaN in its place, 0 elsewhere).
+ * Sums are float32 (a row whose sum, or mean with eps, passes its range is summed in units
+ * of 2^80, so none overflows).  A value that is not finite reaches its own row alone
+ * (NaN: all of it; an infinity: NaN in its place, 0 elsewhere).
  *   r and y may be x or res themselves (element for element); two outputs may not
  * share memory.
  *   eps finite, at least 1e-30 (MOE_ERR_ARG: below, float32 squares would lose digits);
