@@ -256,8 +256,12 @@ __device__ __forceinline__ bool nth_pass(const int32_t* offsets, int E_l, int sl
 // four waves take the units of the reduction (UB blocks of 128) in turn, and their sums meet
 // in LDS for each group.  With UW units to a wave at most (0: any number) it keeps its part of
 // the rows in registers over the groups: read, and for the second product quantised, once.
-// Each of BUF buffers is filled with the weights of the unit that will use it next as soon as
-// its last ones are used: no weights are moved between registers, which would wait for them.
+// With all of a wave's rows held, each of BUF buffers is filled with the weights of the unit that
+// will use it next as soon as its last ones are used.  Where a wave has more units (UW = 0), or
+// one of two, the second buffer's weights are moved to the first, which waits for them, and with
+// UW = 0 a unit's rows are read, and for the second product quantised, where they are used, with no
+// load of them in flight: 2.5 TB/s of weights (16 experts of 4096 x 1024 at 8 rows, 39 us) where
+// held rows give 4.2.
 template <int S, int G, int UW, int UB, bool LOOP, class Op>
 __global__ __launch_bounds__(64 * WAVES) void fp4_small_kernel(
     Op op, WRows4 W, const int32_t* __restrict__ offsets, int E_l, int groups, int span,
@@ -397,14 +401,43 @@ __global__ __launch_bounds__(64 * WAVES) void fp4_small_kernel(
 // only a skewed load needs, which leave at once in others.
 constexpr int kBlocks = 512, kMostBlocks = 4096;
 
+// Whether the kernel's registers, as compiled, leave two waves to a SIMD.
+template <class Op>
+constexpr bool two_waves(int S, int G, int UW, int UB) {
+  if (UB == 1) return !(Op::WIDE && S == 4 && G == 4);
+  if (Op::H == 2) return G < 4 || UW == 0 || (UW == 1 && !Op::WIDE);
+  return G == 1 || (G == 2 && (S == 1 || UW > 0)) || (G == 4 && S == 1 && UW > 0);
+}
+// The units of a wave whose rows it keeps in registers, if that is all of them, else 0.
+template <class Op>
+int held_units(int G, int k) {
+  const int per_wave = (k + 256 * WAVES - 1) / (256 * WAVES);
+  return per_wave <= (Op::WIDE && G > 1 ? 1 : 2) ? per_wave : 0;
+}
+// Token groups of a pass over a reduction of k: Shape's, halved until two waves fit a SIMD.  In
+// us, one wave / halved: 8 of 64 experts of 2048 x 1408 at 23 rows 37 / 31 (first product) and
+// 37 / 29 (second), 8 of 1152 x 1280 at 32 rows 25.8 / 22.5; fp16: 16 of 1024 x 768 at 32 rows
+// 25.4 / 21.7, 8 of 2048 x 384 at 50 rows 20.3 / 18.8, 8 of 4096 x 2048 at 18 rows 62 / 54.  It
+// costs a little where 32-row passes of the second product become 16: 16 of 2048 x 4096 at 17
+// rows 87 / 96, but 8 of 256 of 7168 x 2304 at 20 rows 170 / 152.  Halving everywhere would be
+// slower where 64-row passes leave two waves: 128 of 128 x 768 at 32 rows 26 / 33.
+template <class Op>
+int pass_groups(const Shape& sh, int k) {
+  int G = sh.G;
+  while (G > 1 && !two_waves<Op>(sh.S, G, k <= 128 * WAVES ? 1 : held_units<Op>(G, k),
+                                 k <= 128 * WAVES ? 1 : 2))
+    G /= 2;
+  return G;
+}
+
 template <class Op>
 int launch(const char* name, const moe_shape* s, const Op& op, const WRows4& W, int cols,
            const int32_t* offsets, hipStream_t st) {
   const Shape sh(s, cols, Op::H == 1);
-  const int groups = (int)sh.grid.x;
+  const int groups = (int)sh.grid.x, G_run = pass_groups<Op>(sh, W.k);
   // passes of an even load: experts that have rows, times the passes over what most have at
   // most (as in Shape; with the mean alone 25 us instead of 23, 8 experts of 2048 x 768, 32 rows)
-  const int64_t pairs = s->T * s->K, rows = 16 * sh.G;
+  const int64_t pairs = s->T * s->K, rows = 16 * G_run;
   const double mean = (double)pairs / (double)s->E;
   const double passes =
       std::max(1.0, s->E_l * -expm1(-mean)) * ceil((mean + 2 * sqrt(mean)) / (double)rows);
@@ -412,11 +445,11 @@ int launch(const char* name, const moe_shape* s, const Op& op, const WRows4& W, 
   const int64_t slots = std::max<int64_t>(1, std::min(pairs, s->E_l));
   const int64_t most = slots + pairs / rows;
   // A grid of fewer passes, whose blocks take further ones, where the pass is of 16 rows and
-  // there may be more than 24.  The loop costs 30 registers and a wave per SIMD, in us with /
-  // without: one token, 128 experts of 2048 x 768 12.0 / 11.8, 100 of 8 of 64 experts of 2048 x
+  // there may be more than 24.  The loop costs 30 registers and often a wave per SIMD, in us
+  // with / without: one token, 128 experts of 2048 x 768 12.0 / 11.8, 100 of 8 of 64 experts of 2048 x
   // 1408 19.5 / 18.9, 200 of them (32 rows) 27.4 / 23.6; but the weights of many experts stream
   // better with it: 64 tokens, 128 experts 75 / 79, 8 of them 40 / 42.
-  const bool loop = sh.G == 1 && most > 24;
+  const bool loop = G_run == 1 && most > 24;
   const int64_t parts = std::min<int64_t>(
       {(int64_t)(kBlocks / passes + 0.5), groups, loop ? groups : kMostBlocks / most});
   const int span = (int)cdiv(groups, std::max<int64_t>(1, parts));
@@ -424,7 +457,7 @@ int launch(const char* name, const moe_shape* s, const Op& op, const WRows4& W, 
   const int64_t y =
       loop ? std::min(most, std::max(2 * (int64_t)ceil(passes), cdiv(1024, x))) : most;
   const dim3 grid((unsigned)x, (unsigned)y);
-  const int per_wave = (W.k + 256 * WAVES - 1) / (256 * WAVES);
+  const int held = held_units<Op>(G_run, W.k);
   auto go = [&](auto kernel) {
     MOE_LAUNCH(name, st, kernel<<<grid, 64 * WAVES, 0, st>>>(op, W, offsets, (int)s->E_l, groups,
                                                              span, (int)most));
@@ -432,26 +465,27 @@ int launch(const char* name, const moe_shape* s, const Op& op, const WRows4& W, 
   };
   auto by_rows = [&](auto S_) {
     constexpr int S = decltype(S_)::value;
-    // as many units' rows in registers as leave two waves to a SIMD
-    auto by_units = [&](auto G_, auto most_, auto loop_) {
-      constexpr int G = decltype(G_)::value, MOST = decltype(most_)::value;
+    auto by_units = [&](auto G_, auto loop_) {
+      constexpr int G = decltype(G_)::value;
       constexpr bool LOOP = decltype(loop_)::value;
-      // one block of 128 to a wave where that is all
-      if (W.k <= 128 * WAVES) return go(fp4_small_kernel<S, G, 1, 1, LOOP, Op>);
-      if (per_wave > MOST) return go(fp4_small_kernel<S, G, 0, 2, LOOP, Op>);
-      if constexpr (MOST == 2)
-        if (per_wave == 2) return go(fp4_small_kernel<S, G, 2, 2, LOOP, Op>);
-      return go(fp4_small_kernel<S, G, 1, 2, LOOP, Op>);
+      constexpr int MOST = Op::WIDE && G > 1 ? 1 : 2;
+      // pass_groups took none of the kernels that are left out
+      if constexpr (two_waves<Op>(S, G, 1, 1))
+        // one block of 128 to a wave where that is all
+        if (W.k <= 128 * WAVES) return go(fp4_small_kernel<S, G, 1, 1, LOOP, Op>);
+      if constexpr (two_waves<Op>(S, G, 0, 2))
+        if (held == 0) return go(fp4_small_kernel<S, G, 0, 2, LOOP, Op>);
+      if constexpr (MOST == 2 && two_waves<Op>(S, G, 2, 2))
+        if (held == 2) return go(fp4_small_kernel<S, G, 2, 2, LOOP, Op>);
+      if constexpr (two_waves<Op>(S, G, 1, 2))
+        if (held == 1) return go(fp4_small_kernel<S, G, 1, 2, LOOP, Op>);
+      return set_error(MOE_ERR_UNSUPPORTED, "%s: no kernel", name);
     };
     typedef std::integral_constant<int, 1> One;
-    typedef std::integral_constant<int, 2> Two;
-    if (sh.G == 4)
-      return by_units(std::integral_constant<int, 4>{},
-                      std::integral_constant<int, Op::WIDE || S == 4 ? 1 : 2>{}, std::false_type{});
-    if (sh.G == 2)
-      return by_units(Two{}, std::integral_constant<int, Op::WIDE ? 1 : 2>{}, std::false_type{});
-    if (loop) return by_units(One{}, Two{}, std::true_type{});
-    return by_units(One{}, Two{}, std::false_type{});
+    if (G_run == 4) return by_units(std::integral_constant<int, 4>{}, std::false_type{});
+    if (G_run == 2) return by_units(std::integral_constant<int, 2>{}, std::false_type{});
+    if (loop) return by_units(One{}, std::true_type{});
+    return by_units(One{}, std::false_type{});
   };
   if constexpr (Op::H == 1)
     if (sh.S == 4) return by_rows(std::integral_constant<int, 4>{});
@@ -476,26 +510,34 @@ int ffn_fwd_t(const moe_shape* s, const void* xq, const uint8_t* xs, const int32
 
 // Few rows: up to 20 per expert on average (17 in fp16), and (x / E_l F d)^2 more with x =
 // 5e7 in bf16 and 7e7 in fp16, 256 at most.  Below it these kernels are faster than the tiles,
-// whose time hardly falls with the rows; above, more than 32 rows of an expert take a pass
-// over its weights each, or more registers than leave two waves to a SIMD.  Both sides in us
-// on an MI355X, forward, small against tiles: bf16, 128 experts of 2048 x 768 at 8 rows 83 / 117,
-// at 16 90 / 117, at 20 123 / 118, at 24 143 / 119; 64 of them at 20 51 / 74, at 24 83 / 75; 16 of
-// 4096 x 1024 at 20 50 / 59, at 25 67 / 60; 8 of 2048 x 1408 at 21 24 / 37, at 26 39 / 37; 8 of
-// 2048 x 768 at 32 24 / 32, at 64 37 / 33; 8 of 1024 x 256 at 184 19 / 24; 4 of 640 x 384 at 256
-// 15 / 25.  fp16: 128 of 2048 x 768 at 16 125 / 150, at 20 165 / 150; 8 of 2048 x 1408 at 21
-// 34 / 55; 8 of 2048 x 768 at 64 47 / 49, at 128 66 / 50.
-// These are even loads.  A fuller expert takes more passes, each over its weights again from
-// L2: 128 experts of 2048 x 768, Zipf 1.1, at 4 rows 62 / 74, at 16 88 / 99; 8 of 64 of 2048 x
-// 1408 at 19 65 / 40; one of 512 of 2048 x 768 at 16 (the fullest, 950 rows) 85 / 34 where its
-// even load is 10 / 30.  So that it stays within a few times the tiles' time, no expert may
+// whose time hardly falls with the rows; above, an expert's rows take several passes, each over
+// its weights again.  Both sides in us on an MI355X, forward, small against tiles: bf16, 128
+// experts of 2048 x 768 at 8 rows 82 / 117, at 16 85 / 117, at 20 118 / 119, at 24 129 / 119; 64
+// of them at 20 49 / 74, at 24 72 / 75; 16 of 4096 x 1024 at 20 49 / 60, at 25 59 / 60, at 32 65 /
+// 60; 8 of 2048 x 1408 at 21 24 / 37, at 26 28 / 38, at 36 34 / 38; 8 of 2048 x 768 at 32 23 / 32,
+// at 64 28 / 33; 8 of 1024 x 256 at 184 18 / 24; 4 of 640 x 384 at 256 14 / 25.  fp16: 128 of 2048
+// x 768 at 16 124 / 150, at 20 165 / 151; 8 of 2048 x 1408 at 26 35 / 54; 8 of 2048 x 768 at 64
+// 42 / 49, at 128 59 / 50.
+// These are even loads, which for few experts would bear a higher border.  It stays below them
+// because a fuller expert takes more passes, each over its weights again from L2, and the
+// loads are not known here: 128 experts of 2048 x 768, Zipf 1.1, at 4 rows 62 / 73, at 16 83 /
+// 99; 8 of 64 of 2048 x 1408 at 9 45 / 39, at 19 64 / 40, at 23 81 / 41; one of 512 of 2048 x
+// 768 at 16 (the fullest, 950 rows) 85 / 34 where its even load is 10 / 30.  So that it stays within a few times the tiles' time, no expert may
 // take more than 64 passes with every token once.
 static int64_t most_mean(const moe_shape* s) {
   const bool bf16 = s->dtype == MOE_BF16;
   const double more = (bf16 ? 5e7 : 7e7) / ((double)s->E_l * (double)s->F * (double)s->d);
   return std::min<int64_t>(256, (bf16 ? 20 : 17) + (int64_t)std::min(256.0, more * more));
 }
+template <typename elt>
+static int64_t least_rows(const moe_shape* s) {
+  const int d = (int)s->d, F = (int)s->F;
+  return 16 * std::min(pass_groups<First<elt>>(Shape(s, F, false), d),
+                       pass_groups<Second<elt>>(Shape(s, d, true), F));
+}
 bool fp4_small(const moe_shape* s) {
-  const int64_t rows = 16 * std::min(Shape(s, (int)s->F, false).G, Shape(s, (int)s->d, true).G);
+  const int64_t rows =
+      s->dtype == MOE_BF16 ? least_rows<uint16_t>(s) : least_rows<_Float16>(s);
   return cdiv(s->T * s->K, s->E) <= most_mean(s) && cdiv(s->T, rows) <= 64;
 }
 // For the longest batch of at most T tokens that these kernels take.
