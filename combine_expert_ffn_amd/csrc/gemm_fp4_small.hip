@@ -401,12 +401,15 @@ __global__ __launch_bounds__(64 * WAVES) void fp4_small_kernel(
 // only a skewed load needs, which leave at once in others.
 constexpr int kBlocks = 512, kMostBlocks = 4096;
 
-// Whether the kernel's registers, as compiled, leave two waves to a SIMD.
+// Whether the kernel's registers, as compiled, leave two waves to a SIMD.  (The second product
+// never meets S = 1 with 64-row passes: in Shape, S = 1 says blocks * cdiv(rows, 16) < 1024, G = 4
+// blocks * cdiv(rows, 64) >= 512 and rows > 32, so cdiv(rows, 16) < 2 cdiv(rows, 64), which no
+// rows > 16 fulfil.)
 template <class Op>
 constexpr bool two_waves(int S, int G, int UW, int UB) {
-  if (UB == 1) return !(Op::WIDE && S == 4 && G == 4);
+  if (UB == 1) return Op::H == 2 || G < 4 || (S == 4 && !Op::WIDE);
   if (Op::H == 2) return G < 4 || UW == 0 || (UW == 1 && !Op::WIDE);
-  return G == 1 || (G == 2 && (S == 1 || UW > 0)) || (G == 4 && S == 1 && UW > 0);
+  return G == 1 || (G == 2 && (S == 1 || UW > 0));
 }
 // The units of a wave whose rows it keeps in registers, if that is all of them, else 0.
 template <class Op>
