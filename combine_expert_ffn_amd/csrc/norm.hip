@@ -6,7 +6,8 @@
 // row is held in the registers of 16, 64 or 256 lanes (d up to 512, 2048, 16384), eight
 // consecutive elements of a lane to a 16-byte load, so the sum of squares needs no
 // second read, and 16 lanes hold a scale block of 128.  Sums are float32: a lane's own,
-// then over the lanes in a fixed order.
+// then over the lanes in a fixed order.  Which products are fused into a sum is written out, so
+// that a row's bits are the same in every kernel (the compiler chose otherwise in some).
 // dgamma is a sum over all rows: a block keeps its columns' sums in registers while
 // it walks its rows, writes one row of them, and a second launch adds those rows in
 // a fixed order.  For few rows dgamma's columns are summed by further blocks of the same
@@ -131,7 +132,7 @@ __global__ __launch_bounds__(NT) void rmsnorm_kernel(Fwd<T> a) {
         float f[8];
         xr[c].unpack(f);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) sum += (f[i] * unit) * (f[i] * unit);
+        for (int i = 0; i < 8; ++i) sum = fmaf(f[i] * unit, f[i] * unit, sum);
       }
       return sum;
     };
@@ -222,7 +223,7 @@ __device__ __forceinline__ void sum_columns(const Bwd<T>& a, int block) {
       dy[u].unpack(f);
       r[u].unpack(x);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) acc[i] += f[i] * (x[i] * rstd[u]);
+      for (int i = 0; i < 8; ++i) acc[i] = fmaf(f[i], x[i] * rstd[u], acc[i]);
     }
   }
 #pragma unroll
@@ -287,8 +288,8 @@ __global__ __launch_bounds__(NT) void rmsnorm_bwd_kernel(Bwd<T> a) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const float xhat = x[i] * rstd;
-        sum += f[i] * g[i] * xhat;
-        acc[c][i] += f[i] * xhat;
+        sum = fmaf(f[i] * g[i], xhat, sum);
+        acc[c][i] = fmaf(f[i], xhat, acc[c][i]);
       }
     }
     const float mean = row_sum<L>(sum, s_sum, turn) / (float)a.d;
@@ -300,7 +301,8 @@ __global__ __launch_bounds__(NT) void rmsnorm_bwd_kernel(Bwd<T> a) {
       gamma[c].unpack(g);
       dres[c].unpack(e);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) f[i] = rstd * (f[i] * g[i] - x[i] * rstd * mean) + e[i];
+      for (int i = 0; i < 8; ++i)
+        f[i] = fmaf(rstd, fmaf(-(x[i] * rstd), mean, f[i] * g[i]), e[i]);
       Raw8<T> o;
       o.pack(f);
       if (on && c * L + lane < chunks) o.template store<PAST>(a.dx + at + (c * L + lane) * 8);

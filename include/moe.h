@@ -635,7 +635,8 @@ int moe_ffn_dgrad_fp8(const moe_shape* s, const void* dq, const uint8_t* ds,
  * of 2^80, so none overflows).  A value that is not finite reaches its own row alone
  * (NaN: all of it; an infinity: NaN in its place, 0 elsewhere).
  *   r and y may be x or res themselves (element for element); two outputs may not
- * share memory.
+ * share memory.  A row's results depend on that row, gamma, eps and dtype alone, bit for
+ * bit, here and in the backward pass (dx).
  *   eps finite, at least 1e-30 (MOE_ERR_ARG: below, float32 squares would lose digits);
  * q needs d to be a multiple of 128 (MOE_ERR_SHAPE).
  * All pointers 16-byte aligned but qs and rstd, which are 4-byte (MOE_ERR_ARG).  With
@@ -659,7 +660,8 @@ size_t moe_rmsnorm_workspace_bytes(const moe_shape* s);
  *   r [T,d] (x where there was no res), rstd [T] f32 from moe_rmsnorm
  *   dx [T,d] out (dtype); may be dy, dres or r itself
  *   dgamma [d] f32 out or NULL (ws may then be NULL); accumulate & MOE_ACCUM_DW adds
- *   to the existing values, otherwise T = 0 gives 0.  Summed in a fixed order.
+ *   to the existing values, otherwise T = 0 gives 0.  Summed in a fixed order, which
+ *   follows from T, d and whether dx takes the place of dy or r.
  * Alignment as moe_rmsnorm; dgamma and ws 16-byte.
  */
 int moe_rmsnorm_bwd(const moe_shape* s, const void* dy, const void* r, const void* gamma,
