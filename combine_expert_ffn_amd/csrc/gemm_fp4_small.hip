@@ -16,7 +16,7 @@
 // MFMAs.
 // 128 experts of 2048 x 768, bf16, both products: one token (8 experts, 20 MB) 11.8 us, two
 // launches of 6.5 and 5.0 whose chains of latencies (plan, weights, sum over waves) bound
-// them; 64 tokens (316 MB) 75 us, 4.2 TB/s of weights; 256 tokens 90.
+// them; 64 tokens (316 MB) 75 us, 4.2 TB/s of weights; 256 tokens 85.
 #include "moe_fp4.h"
 #include "moe_small8.h"
 

@@ -9,9 +9,9 @@ namespace moe {
 // lanes to a row.
 inline int norm_lanes(int64_t d) { return d <= 512 ? 16 : (d <= 2048 ? 64 : 256); }
 // Blocks of the backward pass, each of which leaves one row of partial sums of
-// dgamma in the workspace: four per CU at most, and, past one per CU, fewer than let each
-// walk over 16 rows (8 rows of more than 2048), since a row of sums in float32 is twice a
-// row of the input.  In us, dx and dgamma together, bf16, with a block for every row or four of
+// dgamma in the workspace: four per CU at most, and, past one per CU, so many that each
+// walks over 64 rows of up to 512, 16 of up to 2048 or 8 of more, since a row of sums in
+// float32 is twice a row of the input.  In us, dx and dgamma together, bf16, with a block for every row or four of
 // up to 2048 / with these: 1500 x 4096 26 / 16, 4096 x 4096 32 / 27, 2048 x 16384 99 / 52, 4096 x
 // 2048 19 / 16; 16 rows where it is 8: 1500 x 4096 17.  8192 x 640: 11.3 / 11.0, with 32 rows 13.6.
 constexpr int64_t kNormParts = 1024;

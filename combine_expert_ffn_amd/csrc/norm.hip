@@ -2,7 +2,10 @@
 // the 8-bit rows behind it, and its backward pass (formulas in moe.h).
 // Both are one pass over memory, which bounds them: 65536 x 2048 bf16 forward with
 // residual, y and 8-bit rows 203 us (1.21 GB, 6.0 TB/s; 222 through the caches and with
-// 2048 blocks), backward with the residual's gradient 183 us (1.07 GB, 5.9 TB/s; 202).  A
+// 2048 blocks), backward with the residual's gradient 183 us (1.07 GB, 5.9 TB/s; 202).  Not
+// the backward of rows of more than 8192: a lane's eight chunks of dy, r, dres, gamma and
+// dgamma leave one wave to a SIMD, so a row's loads, sum and stores follow each other: 8192 x
+// 16384 bf16 235 us (3.4 TB/s), where as many values in rows of 2048 take 141.  A
 // row is held in the registers of 16, 64 or 256 lanes (d up to 512, 2048, 16384), eight
 // consecutive elements of a lane to a 16-byte load, so the sum of squares needs no
 // second read, and 16 lanes hold a scale block of 128.  Sums are float32: a lane's own,
