@@ -1,6 +1,6 @@
 """The norm and the 4-bit experts on another stream than the current one, and two calls at once on
 two streams: inputs, outputs and workspaces are made on the current stream, which the others
-wait for before the calls."""
+wait for before the calls.  And long batches in captured graphs that share a workspace."""
 
 import pytest
 import torch
@@ -66,3 +66,38 @@ def test_experts(name, dtype):
         o["y"], ws, st) for o, ws in zip(outs, spaces)])
     for o in outs:
         assert all(torch.equal(o[n], want[n]) for n in want)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("T,d", [(1500, 640), (5000, 2048), (1100, 8320)])
+def test_norm_graphs_share_a_workspace(T, d, dtype):
+    """dgamma's partial sums of two captured backward passes in one workspace, which eager work
+    overwrites between the replays."""
+    n, other = Norm(T, d, dtype, q=False), Norm(T, d, dtype, q=False, seed=1)
+    calls, outs = [], []
+    for m in (n, other):
+        o = m.out()
+        dx, dg = torch.empty_like(m.x), torch.empty(d, device="cuda")
+        outs.append((o["r"], o["y"], o["rstd"], dx, dg))
+        calls.append(lambda m=m, o=o, dx=dx, dg=dg: (m.forward(o), M.moe_rmsnorm_bwd(
+            m.s, m.dy, o["r"], m.gamma, o["rstd"], m.dres, dx, dg, 0, n.ws)))
+    for call in calls:
+        call()
+    torch.cuda.synchronize()
+    graphs = [torch.cuda.CUDAGraph() for _ in calls]
+    for graph, call in zip(graphs, calls):
+        with torch.cuda.graph(graph):
+            call()
+    for k in range(3):
+        for m in (n, other):
+            m.x.copy_(torch.randn_like(m.x.float()))
+            m.dy.copy_(torch.randn_like(m.x.float()))
+        for graph in graphs if k % 2 else graphs[::-1]:
+            graph.replay()
+        torch.cuda.synchronize()
+        got = [[t.clone() for t in out] for out in outs]
+        n.ws.fill_(255)
+        for call, out, was in zip(calls, outs, got):
+            call()
+            torch.cuda.synchronize()
+            assert all(torch.equal(a, b) for a, b in zip(out, was)), k
