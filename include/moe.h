@@ -700,7 +700,8 @@ int moe_quant_weights_fp4(const moe_shape* s, const void* W_gu, const void* W_do
                           const moe_fp4_weights* w, hipStream_t stream);
 
 /* moe_dequant_weights_fp4 - the values that w stands for, rounded to dtype: exact in
- * MOE_F32, and in the 16-bit types within their range.  moe_ffn_dgrad on them is the
+ * MOE_F32 below 2^128, and in the 16-bit types within their range (a weight above 7 * 2^125,
+ * quantised to 4 * 2^126, reads back as an infinity).  moe_ffn_dgrad on them is the
  * gradient of moe_expert_ffn_fwd_fp4 (the quantisation of rows passed straight through). */
 int moe_dequant_weights_fp4(const moe_shape* s, const moe_fp4_weights* w, void* W_gu,
                             void* W_down, hipStream_t stream);
