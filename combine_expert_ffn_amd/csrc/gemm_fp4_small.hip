@@ -449,9 +449,9 @@ int launch(const char* name, const moe_shape* s, const Op& op, const WRows4& W, 
   const int64_t most = slots + pairs / rows;
   // A grid of fewer passes, whose blocks take further ones, where the pass is of 16 rows and
   // there may be more than 24.  The loop costs 30 registers and often a wave per SIMD, in us
-  // with / without: one token, 128 experts of 2048 x 768 12.0 / 11.8, 100 of 8 of 64 experts of 2048 x
-  // 1408 19.5 / 18.9, 200 of them (32 rows) 27.4 / 23.6; but the weights of many experts stream
-  // better with it: 64 tokens, 128 experts 75 / 79, 8 of them 40 / 42.
+  // with / without: one token, 128 experts of 2048 x 768 12.0 / 11.8, 100 of 8 of 64 experts
+  // of 2048 x 1408 19.5 / 18.9, 200 of them (32 rows) 27.4 / 23.6; but the weights of many
+  // experts stream better with it: 64 tokens, 128 experts 75 / 79, 8 of them 40 / 42.
   const bool loop = G_run == 1 && most > 24;
   const int64_t parts = std::min<int64_t>(
       {(int64_t)(kBlocks / passes + 0.5), groups, loop ? groups : kMostBlocks / most});
@@ -525,22 +525,19 @@ int ffn_fwd_t(const moe_shape* s, const void* xq, const uint8_t* xs, const int32
 // because a fuller expert takes more passes, each over its weights again from L2, and the
 // loads are not known here: 128 experts of 2048 x 768, Zipf 1.1, at 4 rows 62 / 73, at 16 83 /
 // 99; 8 of 64 of 2048 x 1408 at 9 45 / 39, at 19 64 / 40, at 23 81 / 41; one of 512 of 2048 x
-// 768 at 16 (the fullest, 950 rows) 85 / 34 where its even load is 10 / 30.  So that it stays within a few times the tiles' time, no expert may
-// take more than 64 passes with every token once.
+// 768 at 16 (the fullest, 950 rows) 85 / 34 where its even load is 10 / 30.  So that
+// it stays within a few times the tiles' time, no expert may take more than 64 passes of
+// Shape's rows with every token once.  (Passes that pass_groups halves count as one: with them
+// counted apart, even loads would go to slower tiles, 128 experts of 128 x 384, fp16, at 38 rows
+// 18 / 32, 256 of 512 of 128 x 1408 at 10 57 / 119, 32 of 256 of 1920 x 256 at 25 23 / 41; the most
+// skewed to faster ones, 16 of 512 of 1152 x 2816, Zipf 1.1, 501 / 158.)
 static int64_t most_mean(const moe_shape* s) {
   const bool bf16 = s->dtype == MOE_BF16;
   const double more = (bf16 ? 5e7 : 7e7) / ((double)s->E_l * (double)s->F * (double)s->d);
   return std::min<int64_t>(256, (bf16 ? 20 : 17) + (int64_t)std::min(256.0, more * more));
 }
-template <typename elt>
-static int64_t least_rows(const moe_shape* s) {
-  const int d = (int)s->d, F = (int)s->F;
-  return 16 * std::min(pass_groups<First<elt>>(Shape(s, F, false), d),
-                       pass_groups<Second<elt>>(Shape(s, d, true), F));
-}
 bool fp4_small(const moe_shape* s) {
-  const int64_t rows =
-      s->dtype == MOE_BF16 ? least_rows<uint16_t>(s) : least_rows<_Float16>(s);
+  const int64_t rows = 16 * std::min(Shape(s, (int)s->F, false).G, Shape(s, (int)s->d, true).G);
   return cdiv(s->T * s->K, s->E) <= most_mean(s) && cdiv(s->T, rows) <= 64;
 }
 // For the longest batch of at most T tokens that these kernels take.

@@ -81,6 +81,24 @@ def test_forward(T, d, F, E, E_l, K, dtype, one):
     A.check_forward(A.forward())
 
 
+@pytest.mark.parametrize("T,d,F,E,E_l,K,dtype", [
+    (2437, 128, 384, 128, 128, 2, "f16"), (2964, 256, 128, 64, 64, 2, "f16"),
+    (3045, 1536, 512, 32, 4, 2, "bf16")])
+def test_long_batches_that_are_few_rows_to_an_expert(T, d, F, E, E_l, K, dtype):
+    """Passes shorter than the launch shape's do not send a batch to the tiles."""
+    A = Layer4(T, d, F, E, 0, E_l, K, dtype, True)
+    M.moe_timing_enable()
+    try:
+        M.moe_timing_reset()
+        out = A.forward()
+        torch.cuda.synchronize()
+        names = set(M.moe_timing_report())
+    finally:
+        M.moe_timing_disable()
+    assert len(names) == 2 and all(n.endswith("_small") for n in names), names
+    A.check_forward(out)
+
+
 NUMBERS = r"fp4_small_kernelILi(\d)ELi(\d)ELi(\d)ELi(\d)ELb(\d)ENS0_\d(First|Second)I(t|DF16_)E"
 NAMES = (r"fp4_small_kernel<(\d), (\d), (\d), (\d), (false|true), .*?(First|Second)"
          r"<(unsigned short|_Float16)>")
