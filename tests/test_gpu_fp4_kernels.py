@@ -81,12 +81,15 @@ def test_forward(T, d, F, E, E_l, K, dtype, one):
     A.check_forward(A.forward())
 
 
+@pytest.mark.parametrize("one", [False, True], ids=["even", "one_expert"])
 @pytest.mark.parametrize("T,d,F,E,E_l,K,dtype", [
     (2437, 128, 384, 128, 128, 2, "f16"), (2964, 256, 128, 64, 64, 2, "f16"),
     (3045, 1536, 512, 32, 4, 2, "bf16")])
-def test_long_batches_that_are_few_rows_to_an_expert(T, d, F, E, E_l, K, dtype):
-    """Passes shorter than the launch shape's do not send a batch to the tiles."""
-    A = Layer4(T, d, F, E, 0, E_l, K, dtype, True)
+def test_long_batches_that_are_few_rows_to_an_expert(T, d, F, E, E_l, K, dtype, one):
+    """Passes shorter than the launch shape's do not send a batch to the tiles; up to 191 of them
+    over one expert that every token names."""
+    A = Layer4(T, d, F, E, 0, E_l, K, dtype, True, only=[2] if one else None)
+    assert not one or A.off[3] - A.off[2] == T
     M.moe_timing_enable()
     try:
         M.moe_timing_reset()
